@@ -412,6 +412,103 @@ qsa_status_t qsa_forward_noalloc(const void* q, const void* k, const void* v, co
                                  int64_t T, int64_t T_kv, int H, int G, int n_sel, float scale,
                                  void* out, float* lse, qsa_stream_t stream);
 
+/*
+ * Serving from a paged K/V cache: rotary positions, the write of new K/V rows
+ * into pages, and attention of new tokens over them.  The pages have no
+ * counterpart of these calls (they name decode over a paged cache as inference
+ * work outside the attention API, "Finding QSA attention and its indexer").
+ *
+ * A cache is
+ *   k_pages, v_pages [n_pages, page_size, G, 256] BF16 (pools)
+ *   block_table [B, max_pages] int32 : page IDs; position j of sequence b is
+ *       row j % page_size of page block_table[b, j / page_size]
+ *   kv_len [B] int32   : tokens that sequence b holds, its new ones included
+ *   cu_q [B + 1] int32 : sequence b's new tokens are the packed rows
+ *       [cu_q[b], cu_q[b + 1]) (ascending offsets, any of them empty); row t of
+ *       them sits at position kv_len[b] - (cu_q[b + 1] - t)
+ * and T packed rows.  These arrays are read on the device only, so their values
+ * are never errors: rows of no sequence (t < cu_q[0], or behind the last one)
+ * are left as they were in every output; a position outside [0, max_pages *
+ * page_size) or on a page ID outside [0, n_pages) has no row: nothing is
+ * written for it and no query sees it.  A page may be shared by sequences that
+ * only read it; two rows of one call must not be appended to the same place.
+ * Several streams may read one cache at once; a call that writes it has to be
+ * ordered against the others by the caller.
+ *   page_size: a power of two, 16 or more (else QSA_ERR_UNSUPPORTED); n_pages *
+ *   page_size and max_pages * page_size at most 2^31 - 1; B >= 1; 1 <= T <= 2^30;
+ *   T * H <= 2^31 - 1; H = 12 G.
+ * Other conventions (alignment, workspace, stream, errors) as at the top.
+ */
+
+/*
+ * Rotary positions.  Pair i < rotary_dim / 2 of every head turns by the angle
+ * positions[t] * inv_freq[i] and grows by mscale:
+ *   y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x1 sin a + x2 cos a),
+ * computed in FP32 from angles kept to 2^-32 of a turn, rounded once.  Pair i is
+ * dims (2i, 2i + 1) when `interleaved`, else (i, i + rotary_dim / 2); dims from
+ * rotary_dim up pass unchanged.  With `backward` nonzero the turn is by -a: the
+ * gradient with respect to x from the gradient with respect to y.  Scaled
+ * positions (long contexts) come as the frequencies and the mscale that go with
+ * them.
+ *   q, q_out [T, H, 256], k, k_out [T, G, 256] BF16 with element strides between
+ *   tokens and heads (multiples of 8; dims contiguous; 16-byte aligned).  G = 0:
+ *   no k.  Any H >= 1, G >= 0.  An output is its own input (same pointer and
+ *   strides: in place) or overlaps it nowhere, and its rows do not overlap.
+ *   positions [T] int32 (any value); inv_freq [rotary_dim / 2] double, finite;
+ *   rotary_dim a multiple of 16, at most 256 (else QSA_ERR_UNSUPPORTED);
+ *   0 < mscale < inf.
+ */
+qsa_status_t qsa_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                      int64_t k_token_stride, int64_t k_head_stride, void* q_out, int64_t q_out_token_stride,
+                      int64_t q_out_head_stride, void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                      const int32_t* positions, const double* inv_freq, int64_t T, int H, int G, int rotary_dim,
+                      int interleaved, float mscale, int backward, qsa_stream_t stream);
+
+/*
+ * Writes the packed rows k_new and v_new [T, G, 256] to their positions' rows of
+ * the pools, one launch.  With inv_freq (as in qsa_rope, positions from the
+ * cache) k is rotated on the way, and q [T, H, 256], when given, to q_out (every
+ * row that belongs to a sequence, with or without a page).  inv_freq NULL: k
+ * as it is, and no q (QSA_ERR_INVALID_ARGUMENT with one).  Strides, in-place
+ * rule and errors as in qsa_rope.
+ */
+qsa_status_t qsa_cache_append(const void* k_new, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
+                              int64_t v_token_stride, int64_t v_head_stride, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+                              int64_t q_out_head_stride, const double* inv_freq, int rotary_dim, int interleaved,
+                              float mscale, void* k_pages, void* v_pages, const int32_t* block_table,
+                              const int32_t* kv_len, const int32_t* cu_q, int64_t T, int B, int64_t n_pages,
+                              int page_size, int64_t max_pages, int H, int G, qsa_stream_t stream);
+
+/*
+ * qsa_forward over the pages: routes [T, n_sel] name positions of the row's own
+ * sequence (a set, as there; an ID is valid iff 0 <= r < kv_len and the position
+ * has a row; no causal mask is added).  q, out [T, H, 256] BF16 and lse [T, H]
+ * float32 as in qsa_forward; a row with no valid route gives zero output and -inf
+ * LSE.  K/V rows that a token does not see are never read for it.  Few rows with
+ * long lists are split over the SMs and joined in a fixed order: results are bit
+ * for bit the same from run to run.
+ */
+size_t qsa_paged_forward_workspace_size(int64_t T, int H, int G, int n_sel, int page_size, int64_t max_pages);
+qsa_status_t qsa_paged_forward(const void* q, const void* k_pages, const void* v_pages, const int32_t* routes,
+                               const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_q, int64_t T,
+                               int B, int64_t n_pages, int page_size, int64_t max_pages, int H, int G, int n_sel,
+                               float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                               qsa_stream_t stream);
+
+/*
+ * Attention over the pages by position: the token at position p sees the
+ * positions j <= p of its sequence with j > p - window or j < sinks (window 0:
+ * all j <= p, and sinks has no part).  Outputs, empty rows and errors as in
+ * qsa_paged_forward; window, sinks >= 0.
+ */
+size_t qsa_paged_causal_workspace_size(int64_t T, int H, int G, int page_size, int64_t max_pages, int window,
+                                       int sinks);
+qsa_status_t qsa_paged_causal(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
+                              const int32_t* kv_len, const int32_t* cu_q, int64_t T, int B, int64_t n_pages,
+                              int page_size, int64_t max_pages, int H, int G, int window, int sinks, float scale,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes, qsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

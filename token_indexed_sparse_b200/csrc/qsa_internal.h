@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "qsa_cache.cuh"
+
 namespace qsa {
 
 // Route preprocessing (qsa_routes.cu).
@@ -114,5 +116,34 @@ cudaError_t launch_selector_scores(const void* qi, const void* kbar, int64_t T, 
 cudaError_t launch_selector_topk(const float* scores, int64_t stride, int64_t T, int64_t NB, int k,
                                  const int32_t* pos, const int32_t* blk_base, const int32_t* tok_base,
                                  int32_t* blocks, int32_t* routes, cudaStream_t s);
+
+// Rows of 256-dim BF16 heads: head h of token t at p + t * ts + h * hs elements.
+struct HeadRows {
+  const void* p;
+  int64_t ts, hs;
+};
+// Rotary positions (qsa_rope.cu): q (H heads) and k (G heads, may be 0) of T tokens to qo / ko;
+// `backward` turns the other way.
+cudaError_t launch_rope(const HeadRows& q, const HeadRows& k, const HeadRows& qo, const HeadRows& ko,
+                        const int32_t* positions, const double* inv_freq, int64_t T, int H, int G, int rot, bool inter,
+                        float m, bool backward, cudaStream_t s);
+// New K (rotated) and V rows of a packed batch into their pages, and the nq heads of q rotated to qo.
+cudaError_t launch_cache_append(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& qo,
+                                void* k_pages, void* v_pages, const CacheView& c, const double* inv_freq, int64_t T,
+                                int nq, int G, int rot, bool inter, float m, cudaStream_t s);
+
+// Attention of a packed batch's new tokens over the pages by sorted route lists (qsa_paged.cu):
+// row_cnt / row_cols as launch_route_rows writes them for IDs below max_pages * page_size.
+// `splits` parts of every row's keys go to `partial` (paged_partial_bytes) and
+// are joined when it is above 1.
+int paged_splits(int64_t T, int G, int64_t max_keys);
+size_t paged_partial_bytes(int64_t T, int G, int splits);
+cudaError_t launch_paged_forward(const void* q, const void* k_pages, const void* v_pages, const CacheView& c,
+                                 const int32_t* row_cnt, const int32_t* row_cols, int64_t T, int G, int n_sel,
+                                 float scale, int splits, void* partial, void* out, float* lse, cudaStream_t s);
+// The same over the keys j <= position with j > position - window (when window > 0) or j < sinks.
+cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* v_pages, const CacheView& c, int64_t T,
+                                int G, int window, int sinks, float scale, int splits, void* partial, void* out,
+                                float* lse, cudaStream_t s);
 
 }  // namespace qsa

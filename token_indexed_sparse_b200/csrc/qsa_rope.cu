@@ -1,0 +1,219 @@
+// Rotary positions, their gradient, and the write of new K/V rows into a paged
+// cache with the rotation on the way.
+//
+// Pair i of a head turns by the angle pos * f_i and grows by m:
+//   y1 = m (x1 cos a - x2 sin a),  y2 = m (x1 sin a + x2 cos a),
+// pairs being dims (2i, 2i + 1) (interleaved) or (i, i + R / 2) (half layout),
+// i < R / 2; dims R and up pass unchanged.  The map is m times a rotation, so
+// the gradient is m times the opposite rotation: the same kernel with -sin.
+//
+// Angles: pos * f_i reaches 1e6 radians, where 32 bits keep 0.06 of a radian.
+// The turn count f_i / (2 pi) mod 1 is taken once in 64-bit floating point as a
+// fraction of 2^64; times the integer position, modulo 2^64, it is the angle's
+// fraction of a turn with no range reduction, and its top 32 bits as half-turns
+// go to sincospi (error about 1e-7 of a radian).
+//
+// Bound by memory: every 16-byte piece is read and written once.  A block takes
+// kTok tokens; each thread first issues the loads of its pieces, then computes one
+// (token, pair) cosine and sine into shared memory for all heads, then rotates
+// in FP32 and rounds once.  A thread's unit is two 16-byte pieces of one head
+// that hold eight whole pairs in either layout, so both layouts move whole
+// 16-byte pieces.
+#include "qsa_cache.cuh"
+#include "qsa_device.cuh"
+#include "qsa_internal.h"
+
+namespace qsa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kTok = 2;                          // tokens per block
+constexpr int kUnits = kHeadDim / 16;            // two-piece units per head
+constexpr int kAhead = 4;                        // units whose loads a thread holds
+constexpr int kCsUnit = 9;                       // a unit's eight (cos, sin) and one of padding: no bank conflicts
+constexpr double kInvTwoPi = 0.15915494309189533577;
+
+// Fraction of a turn of one position step, in units of 2^-64.
+__device__ __forceinline__ unsigned long long turn_step(double f) {
+  const double t = f * kInvTwoPi;
+  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+}
+
+// cos and sin of pos * f, times m.
+__device__ __forceinline__ float2 turned(double f, int64_t pos, float m) {
+  const unsigned long long a = turn_step(f) * static_cast<unsigned long long>(pos);
+  const int top = static_cast<int>((a + 0x80000000ull) >> 32);  // signed: [-1/2, 1/2) of a turn
+  float s, c;
+  sincospif(static_cast<float>(top) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31: half-turns
+  return make_float2(c * m, s * m);
+}
+
+// The two 16-byte pieces (indices within the head's 32) of unit j.
+__device__ __forceinline__ int2 unit_pieces(int j, int rot, bool inter) {
+  return !inter && j < rot / 16 ? make_int2(j, j + rot / 16) : make_int2(2 * j, 2 * j + 1);
+}
+
+// Rotates unit j's eight pairs: cs[0..8) are their (cos, sin) m.
+__device__ __forceinline__ void rotate_unit(uint4& a, uint4& b, const float2* cs, bool inter, float sign) {
+  uint32_t* pa = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* pb = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (inter) {  // each 32-bit word is a pair
+      const float2 ca = cs[i], cb = cs[4 + i];
+      const float a1 = bf16_lo(pa[i]), a2 = bf16_hi(pa[i]), b1 = bf16_lo(pb[i]), b2 = bf16_hi(pb[i]);
+      const float sa = sign * ca.y, sb = sign * cb.y;
+      pa[i] = pack_bf16(a1 * ca.x - a2 * sa, a1 * sa + a2 * ca.x);
+      pb[i] = pack_bf16(b1 * cb.x - b2 * sb, b1 * sb + b2 * cb.x);
+    } else {  // word i of both pieces: pairs 2i and 2i + 1
+      const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
+      const float x0 = bf16_lo(pa[i]), x1 = bf16_hi(pa[i]), y0 = bf16_lo(pb[i]), y1 = bf16_hi(pb[i]);
+      const float s0 = sign * c0.y, s1 = sign * c1.y;
+      pa[i] = pack_bf16(x0 * c0.x - y0 * s0, x1 * c1.x - y1 * s1);
+      pb[i] = pack_bf16(x0 * s0 + y0 * c0.x, x1 * s1 + y1 * c1.x);
+    }
+  }
+}
+
+__device__ __forceinline__ const uint4* piece(const HeadRows& x, int64_t t, int h) {
+  return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.p) + t * x.ts + h * x.hs);
+}
+
+// Rotates q (H heads) and k (G heads) of T tokens.
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(HeadRows q, HeadRows k, HeadRows qo, HeadRows ko, const int32_t* __restrict__ positions,
+            const double* __restrict__ inv_freq, int64_t T, int H, int G, int rot, bool inter, float m, float sign) {
+  __shared__ float2 cs[kTok][kUnits * kCsUnit];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok;
+  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kTok), T - t0));
+  const int units = n_tok * (H + G) * kUnits;
+  for (int u0 = 0; u0 < units; u0 += kAhead * kRopeThreads) {
+    uint4 a[kAhead], b[kAhead];
+    // unit u: token u / ((H + G) kUnits), head, unit of the head
+    auto where = [&](int u, int& tok, int& h, int& j) {
+      j = u % kUnits;
+      const int r = u / kUnits;
+      tok = r / (H + G);
+      h = r - tok * (H + G);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int u = u0 + i * kRopeThreads + threadIdx.x;
+      if (u >= units) continue;
+      int tok, h, j;
+      where(u, tok, h, j);
+      const uint4* x = h < H ? piece(q, t0 + tok, h) : piece(k, t0 + tok, h - H);
+      const int2 pc = unit_pieces(j, rot, inter);
+      a[i] = x[pc.x];
+      b[i] = x[pc.y];
+    }
+    if (u0 == 0) {
+      const int tok = threadIdx.x >> 7, f = threadIdx.x & 127;
+      if (tok < n_tok && f < rot / 2) cs[tok][(f >> 3) * kCsUnit + (f & 7)] = turned(__ldg(inv_freq + f), __ldg(positions + t0 + tok), m);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int u = u0 + i * kRopeThreads + threadIdx.x;
+      if (u >= units) continue;
+      int tok, h, j;
+      where(u, tok, h, j);
+      if (j < rot / 16) rotate_unit(a[i], b[i], cs[tok] + kCsUnit * j, inter, sign);
+      uint4* y = const_cast<uint4*>(h < H ? piece(qo, t0 + tok, h) : piece(ko, t0 + tok, h - H));
+      const int2 pc = unit_pieces(j, rot, inter);
+      y[pc.x] = a[i];
+      y[pc.y] = b[i];
+    }
+  }
+}
+
+// Writes a packed batch's new K (rotated) and V rows into their pages, and the
+// rotated q rows (when nq > 0; nq = H, or 0 without q) to qo.  Rows of no sequence
+// are left alone; a row whose position has no page gets its q but no K/V row.
+__global__ void __launch_bounds__(kRopeThreads)
+append_kernel(HeadRows q, HeadRows k, HeadRows v, HeadRows qo, __nv_bfloat16* __restrict__ k_pages,
+              __nv_bfloat16* __restrict__ v_pages, CacheView c, const double* __restrict__ inv_freq, int64_t T, int nq,
+              int G, int rot, bool inter, float m) {
+  __shared__ float2 cs[kTok][kUnits * kCsUnit];
+  __shared__ int64_t s_pos[kTok];
+  __shared__ int s_row[kTok];  // pool row, -1 without a page, -2 for a row of no sequence
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok;
+  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kTok), T - t0));
+  const int heads = nq + 2 * G;
+  const int units = n_tok * heads * kUnits;
+  for (int u0 = 0; u0 < units; u0 += kAhead * kRopeThreads) {
+    uint4 a[kAhead], b[kAhead];
+    auto where = [&](int u, int& tok, int& h, int& j) {  // heads in the order q, k, v
+      j = u % kUnits;
+      const int r = u / kUnits;
+      tok = r / heads;
+      h = r - tok * heads;
+    };
+    auto pieces = [&](int h, int j) { return unit_pieces(j, h < nq + G ? rot : 0, inter); };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int u = u0 + i * kRopeThreads + threadIdx.x;
+      if (u >= units) continue;
+      int tok, h, j;
+      where(u, tok, h, j);
+      const uint4* x = h < nq ? piece(q, t0 + tok, h)
+                              : (h < nq + G ? piece(k, t0 + tok, h - nq) : piece(v, t0 + tok, h - nq - G));
+      const int2 pc = pieces(h, j);
+      a[i] = x[pc.x];
+      b[i] = x[pc.y];
+    }
+    if (u0 == 0) {
+      if (threadIdx.x < n_tok) {
+        const int seq = cache_seq(c, t0 + threadIdx.x);
+        const int64_t pos = seq < 0 ? 0 : cache_pos(c, seq, t0 + threadIdx.x);
+        s_pos[threadIdx.x] = pos;
+        s_row[threadIdx.x] = seq < 0 ? -2 : cache_row(c, seq, pos);
+      }
+      __syncthreads();
+      const int tok = threadIdx.x >> 7, f = threadIdx.x & 127;
+      if (tok < n_tok && f < rot / 2) cs[tok][(f >> 3) * kCsUnit + (f & 7)] = turned(__ldg(inv_freq + f), s_pos[tok], m);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int u = u0 + i * kRopeThreads + threadIdx.x;
+      if (u >= units) continue;
+      int tok, h, j;
+      where(u, tok, h, j);
+      const int row = s_row[tok];
+      if (row < (h < nq ? -1 : 0)) continue;
+      if (j < rot / 16 && h < nq + G) rotate_unit(a[i], b[i], cs[tok] + kCsUnit * j, inter, 1.f);
+      uint4* y;
+      if (h < nq) {
+        y = const_cast<uint4*>(piece(qo, t0 + tok, h));
+      } else {
+        const int g = h < nq + G ? h - nq : h - nq - G;
+        y = reinterpret_cast<uint4*>((h < nq + G ? k_pages : v_pages) + (static_cast<int64_t>(row) * G + g) * kHeadDim);
+      }
+      const int2 pc = pieces(h, j);
+      y[pc.x] = a[i];
+      y[pc.y] = b[i];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const HeadRows& q, const HeadRows& k, const HeadRows& qo, const HeadRows& ko,
+                        const int32_t* positions, const double* inv_freq, int64_t T, int H, int G, int rot, bool inter,
+                        float m, bool backward, cudaStream_t s) {
+  rope_kernel<<<static_cast<unsigned>((T + kTok - 1) / kTok), kRopeThreads, 0, s>>>(
+      q, k, qo, ko, positions, inv_freq, T, H, G, rot, inter, m, backward ? -1.f : 1.f);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& qo,
+                                void* k_pages, void* v_pages, const CacheView& c, const double* inv_freq, int64_t T,
+                                int nq, int G, int rot, bool inter, float m, cudaStream_t s) {
+  append_kernel<<<static_cast<unsigned>((T + kTok - 1) / kTok), kRopeThreads, 0, s>>>(
+      q, k, v, qo, static_cast<__nv_bfloat16*>(k_pages), static_cast<__nv_bfloat16*>(v_pages), c, inv_freq, T, nq, G,
+      rot, inter, m);
+  return cudaGetLastError();
+}
+
+}  // namespace qsa

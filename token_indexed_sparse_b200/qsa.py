@@ -9,6 +9,7 @@ or the tensors are not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -87,6 +88,20 @@ def library() -> ctypes.CDLL:
     lib.qsa_union_plan.argtypes = [vp, i64, i64, i32, vp, vp, vp, vp, vp, vp]
     lib.qsa_cast_f32_to_bf16.restype = i32
     lib.qsa_cast_f32_to_bf16.argtypes = [vp, vp, i64, vp]
+    rows = [vp, i64, i64]  # a [T, heads, 256] operand: pointer, token and head strides
+    cache = [vp, vp, vp, i64, i32, i64, i32, i64, i32, i32]  # table, kv_len, cu_q, T, B, n_pages, page_size, max_pages, H, G
+    lib.qsa_rope.restype = i32
+    lib.qsa_rope.argtypes = rows * 4 + [vp, vp, i64, i32, i32, i32, i32, f32, i32, vp]
+    lib.qsa_cache_append.restype = i32
+    lib.qsa_cache_append.argtypes = rows * 4 + [vp, i32, i32, f32, vp, vp] + cache + [vp]
+    lib.qsa_paged_forward_workspace_size.restype = sz
+    lib.qsa_paged_forward_workspace_size.argtypes = [i64, i32, i32, i32, i32, i64]
+    lib.qsa_paged_forward.restype = i32
+    lib.qsa_paged_forward.argtypes = [vp] * 4 + cache + [i32, f32, vp, vp, vp, sz, vp]
+    lib.qsa_paged_causal_workspace_size.restype = sz
+    lib.qsa_paged_causal_workspace_size.argtypes = [i64, i32, i32, i32, i64, i32, i32]
+    lib.qsa_paged_causal.restype = i32
+    lib.qsa_paged_causal.argtypes = [vp] * 3 + cache + [i32, i32, f32, vp, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -410,3 +425,246 @@ def select(qi, kbar, scale: float, k: int, pos=None, blk_base=None, tok_base=Non
     blocks, routes = selector_topk(scores, k, kbar.shape[0], pos, blk_base, tok_base)
     return scores, blocks, routes, status
 
+
+# ---------------------------------------------------------------------------
+# serving from a paged K/V cache
+# ---------------------------------------------------------------------------
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     original_len: int = 4096, fast_turns: float = 32.0, slow_turns: float = 1.0, device="cuda"):
+    """``(inv_freq [rotary_dim / 2] float64 on device, mscale)`` for ``rope`` and ``cache_append``.
+
+    Pair i turns by ``base ** (-2 i / rotary_dim)`` per position.  ``scaling``
+    for contexts ``factor`` times ``original_len``: ``"linear"`` divides every
+    frequency by the factor; ``"yarn"`` (Peng et al., 2023) divides those of
+    pairs with fewer than ``slow_turns`` turns over the original length, keeps
+    those with more than ``fast_turns``, goes linearly in the number of pairs
+    between, and grows q and k by ``0.1 ln(factor) + 1``."""
+    if rotary_dim < 16 or rotary_dim > 256 or rotary_dim % 16:
+        raise ValueError("rotary_dim must be a multiple of 16, at most 256")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    inv_freq, mscale = base ** (-2.0 * i / rotary_dim), 1.0
+    if scaling == "linear":
+        inv_freq = inv_freq / factor
+    elif scaling == "yarn":
+        def pair(turns):  # the (real) pair index that makes this many turns over the original length
+            return rotary_dim * math.log(original_len / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
+        if not fast_turns > slow_turns > 0.0 or original_len < 1:
+            raise ValueError("yarn needs fast_turns > slow_turns > 0 and original_len >= 1")
+        lo, hi = math.floor(pair(fast_turns)), math.ceil(pair(slow_turns))
+        lo, hi = max(lo, 0), min(hi, rotary_dim - 1)
+        slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        inv_freq = inv_freq * (1.0 - slow) + inv_freq / factor * slow
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling is not None:
+        raise ValueError('scaling must be None, "linear" or "yarn"')
+    return inv_freq.to(device), mscale
+
+
+def _on(device: torch.device, what: str, **tensors):
+    """All tensors (None: absent) on the CUDA device of the call."""
+    if device.type != "cuda":
+        raise ValueError(f"{what}: tensors must be CUDA tensors")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _enqueue(device: torch.device, what: str, call, *args):
+    """Runs a library call with ``device`` current, its stream last in the arguments."""
+    if device.index == torch.cuda.current_device():
+        _check(call(*args, _stream(device)), what)
+        return
+    with torch.cuda.device(device):
+        _check(call(*args, _stream(device)), what)
+
+
+def _rows(x: torch.Tensor, T: int | None, name: str):
+    """Pointer and strides of a ``[T, heads, 256]`` BF16 operand (dims contiguous, the rest as it is)."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 3 or x.shape[2] != 256 or (T is not None and x.shape[0] != T):
+        raise ValueError(f"{name} must be [{'T' if T is None else T}, heads, 256], got {tuple(x.shape)}")
+    if x.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous dims")
+    # the stride of an axis of length one is free
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0
+
+
+def _rows_out(x: torch.Tensor, out: torch.Tensor | None, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def _frequencies(inv_freq: torch.Tensor) -> int:
+    """Checks the rotary frequencies; returns rotary_dim."""
+    if inv_freq.dtype != torch.float64:
+        raise TypeError(f"inv_freq must be {torch.float64}, got {inv_freq.dtype}")
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous vector of rotary_dim / 2 frequencies")
+    return 2 * inv_freq.numel()
+
+
+def _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, backward, what):
+    lib = library()
+    T, H = q.shape[:2] if q.dim() == 3 else (0, 0)
+    out_q = _rows_out(q, out_q, "out_q")
+    rows = [*_rows(q, None, "q"), 0, 0, 0, *_rows(out_q, T, "out_q"), 0, 0, 0]
+    G = 0
+    if k is not None:
+        out_k = _rows_out(k, out_k, "out_k")
+        rows[3:6], rows[9:12] = _rows(k, T, "k"), _rows(out_k, T, "out_k")
+        G = k.shape[1]
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    if positions.dtype != torch.int32:
+        raise TypeError(f"positions must be {torch.int32}, got {positions.dtype}")
+    if positions.shape != (T,) or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous [{T}] vector")
+    rot = _frequencies(inv_freq)
+    _on(q.device, what, k=k, out_q=out_q, out_k=out_k, positions=positions, inv_freq=inv_freq)
+    _enqueue(q.device, what, lib.qsa_rope, *rows, positions.data_ptr(), inv_freq.data_ptr(), T, H, G, rot,
+             1 if interleaved else 0, mscale, backward)
+    return out_q, out_k
+
+
+def rope(q, k, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0, out_q=None, out_k=None):
+    """qsa_rope: ``(q', k')``, q ``[T, H, 256]`` and k ``[T, G, 256]`` (or None) turned to their positions.
+
+    ``positions`` [T] int32, ``inv_freq`` [rotary_dim / 2] float64 and
+    ``mscale`` as from ``rope_frequencies``; dims from rotary_dim up pass.  q and k
+    may be slices of one projection (any strides between tokens and heads that
+    are multiples of 8); ``out_q`` / ``out_k`` may be the inputs (in place)."""
+    return _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, 0, "qsa_rope")
+
+
+def rope_backward(grad_q, grad_k, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0,
+                  out_q=None, out_k=None):
+    """The gradient of ``rope``: ``(dq, dk)`` from the gradients of its outputs (the opposite turn)."""
+    return _rope(grad_q, grad_k, positions, inv_freq, interleaved, mscale, out_q, out_k, 1, "qsa_rope")
+
+
+def _cache(k_pages, v_pages, block_table, kv_len, cu_q, T: int, H: int):
+    """Checks a cache; returns the arguments (table, kv_len, cu_q, T, B, n_pages, page_size, max_pages, H, G)."""
+    for x, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if x.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+        if x.dim() != 4 or x.shape[3] != 256 or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [n_pages, page_size, G, 256] tensor")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    for x, name in ((block_table, "block_table"), (kv_len, "kv_len"), (cu_q, "cu_q")):
+        if x.dtype != torch.int32:
+            raise TypeError(f"{name} must be {torch.int32}, got {x.dtype}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    if kv_len.shape != (B,) or cu_q.shape != (B + 1,):
+        raise ValueError(f"kv_len must be [{B}] and cu_q [{B + 1}]")
+    n_pages, page_size, G, _ = k_pages.shape
+    return (block_table.data_ptr(), kv_len.data_ptr(), cu_q.data_ptr(), T, B, n_pages, page_size, max_pages, H, G)
+
+
+def cache_append(k_new, v_new, k_pages, v_pages, block_table, kv_len, cu_q, *, q=None, inv_freq=None,
+                 interleaved: bool = False, mscale: float = 1.0, out_q=None):
+    """qsa_cache_append: writes the new tokens' K and V rows ``[T, G, 256]`` into the pages (in place).
+
+    With ``inv_freq`` (see ``rope_frequencies``) k is turned to its position in
+    the cache first, and ``q`` [T, H, 256] with it: returns the turned q (into
+    ``out_q``, which may be q itself), else None."""
+    lib = library()
+    T, G = k_new.shape[:2] if k_new.dim() == 3 else (0, 0)
+    H = 12 * G
+    rows = [*_rows(k_new, None, "k_new"), *_rows(v_new, T, "v_new"), 0, 0, 0, 0, 0, 0]
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have one shape")
+    if q is not None:
+        if inv_freq is None:
+            raise ValueError("q is only taken to be rotated: it needs inv_freq")
+        out_q = _rows_out(q, out_q, "out_q")
+        rows[6:9], rows[9:12] = _rows(q, T, "q"), _rows(out_q, T, "out_q")
+        H = q.shape[1]
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
+    if k_pages.shape[2] != G:
+        raise ValueError(f"the pages hold {k_pages.shape[2]} KV heads, k_new {G}")
+    rot = _frequencies(inv_freq) if inv_freq is not None else 0
+    _on(k_new.device, "qsa_cache_append", v_new=v_new, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
+        kv_len=kv_len, cu_q=cu_q, q=q, inv_freq=inv_freq, out_q=out_q)
+    _enqueue(k_new.device, "qsa_cache_append", lib.qsa_cache_append, *rows,
+             inv_freq.data_ptr() if inv_freq is not None else None, rot, 1 if interleaved else 0, mscale,
+             k_pages.data_ptr(), v_pages.data_ptr(), *cache)
+    return out_q
+
+
+def _paged_io(q, k_pages, out, lse):
+    q = _prep(q, torch.bfloat16, "q")
+    if q.dim() != 3 or q.shape[2] != 256:
+        raise ValueError(f"q must be [T, H, 256], got {tuple(q.shape)}")
+    out = torch.empty_like(q) if out is None else _out(out, q.shape, torch.bfloat16, q.device, "out")
+    lse = (torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse is None
+           else _out(lse, q.shape[:2], torch.float32, q.device, "lse"))
+    return q, out, lse
+
+
+def paged_forward_workspace_size(T, H, G, n_sel, page_size, max_pages) -> int:
+    return int(library().qsa_paged_forward_workspace_size(T, H, G, n_sel, page_size, max_pages))
+
+
+def paged_causal_workspace_size(T, H, G, page_size, max_pages, window: int = 0, sinks: int = 0) -> int:
+    return int(library().qsa_paged_causal_workspace_size(T, H, G, page_size, max_pages, window, sinks))
+
+
+def paged_forward(q, k_pages, v_pages, routes, block_table, kv_len, cu_q, scale: float = 1.0 / 16.0, *, out=None,
+                  lse=None, workspace=None):
+    """qsa_paged_forward: ``(out [T, H, 256] bf16, lse [T, H] float32)`` of new tokens over a paged cache.
+
+    ``routes`` [T, n_sel] int32 name positions of the row's own sequence (a set,
+    as in ``forward``).  Pools ``[n_pages, page_size, G, 256]``, ``block_table``
+    [B, max_pages], ``kv_len`` [B] and ``cu_q`` [B + 1] int32.  Rows of no
+    sequence are left as they were in ``out`` and ``lse``."""
+    lib = library()
+    q, out, lse = _paged_io(q, k_pages, out, lse)
+    routes = _prep(routes, torch.int32, "routes")
+    T, H = q.shape[:2]
+    cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
+    if routes.dim() != 2 or routes.shape[0] != T:
+        raise ValueError("routes must have one row per query")
+    n_sel = routes.shape[1]
+    _on(q.device, "qsa_paged_forward", k_pages=k_pages, v_pages=v_pages, routes=routes, block_table=block_table,
+        kv_len=kv_len, cu_q=cu_q)
+    ws = _workspace(lib.qsa_paged_forward_workspace_size(T, H, cache[9], n_sel, cache[6], cache[7]), q.device,
+                    workspace)
+    _enqueue(q.device, "qsa_paged_forward", lib.qsa_paged_forward, q.data_ptr(), k_pages.data_ptr(),
+             v_pages.data_ptr(), routes.data_ptr(), *cache, n_sel, scale, out.data_ptr(), lse.data_ptr(),
+             ws.data_ptr(), ws.numel())
+    return out, lse
+
+
+def paged_causal(q, k_pages, v_pages, block_table, kv_len, cu_q, scale: float = 1.0 / 16.0, *, window: int = 0,
+                 sinks: int = 0, out=None, lse=None, workspace=None):
+    """qsa_paged_causal: ``(out [T, H, 256] bf16, lse [T, H] float32)`` of new tokens over a paged cache.
+
+    A token at position p sees the positions ``j <= p`` of its sequence, with
+    ``window`` above 0 only those with ``j > p - window`` or ``j < sinks``.  The
+    cache as in ``paged_forward``."""
+    lib = library()
+    q, out, lse = _paged_io(q, k_pages, out, lse)
+    T, H = q.shape[:2]
+    cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
+    _on(q.device, "qsa_paged_causal", k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
+        cu_q=cu_q)
+    ws = _workspace(lib.qsa_paged_causal_workspace_size(T, H, cache[9], cache[6], cache[7], window, sinks), q.device,
+                    workspace)
+    _enqueue(q.device, "qsa_paged_causal", lib.qsa_paged_causal, q.data_ptr(), k_pages.data_ptr(),
+             v_pages.data_ptr(), *cache, window, sinks, scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+             ws.numel())
+    return out, lse
