@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kMaxSel = 16384;
 constexpr int kMinPage = 16;
+constexpr int64_t kMaxLen = int64_t{1} << 30;  // positions that a block table can name
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -35,7 +36,7 @@ qsa_status_t check_heads(int64_t T, int H, int G) {
 qsa_status_t check_cache(int B, int64_t n_pages, int page_size, int64_t max_pages) {
   if (B < 1 || n_pages < 1 || page_size < 1 || max_pages < 1) return QSA_ERR_INVALID_ARGUMENT;
   if (page_size < kMinPage || (page_size & (page_size - 1)) != 0) return QSA_ERR_UNSUPPORTED;
-  if (n_pages > INT32_MAX / page_size || max_pages > INT32_MAX / page_size) return QSA_ERR_INVALID_ARGUMENT;
+  if (n_pages > INT32_MAX / page_size || max_pages > kMaxLen / page_size) return QSA_ERR_INVALID_ARGUMENT;
   return QSA_OK;
 }
 
@@ -108,13 +109,6 @@ qsa_status_t check_paged(int64_t T, int H, int G, int n_sel, int page_size, int6
   QSA_CHECK(check_heads(T, H, G));
   if (n_sel < 1 || n_sel > kMaxSel || T > INT32_MAX / n_sel) return QSA_ERR_INVALID_ARGUMENT;
   return check_cache(1, 1, page_size, max_pages);
-}
-
-// Parts of a row's keys in qsa_paged_causal: by the longest list that its arguments allow.
-int causal_splits(int64_t T, int G, int page_size, int64_t max_pages, int window, int sinks) {
-  int64_t keys = max_pages * page_size;
-  if (window > 0 && static_cast<int64_t>(window) + sinks < keys) keys = static_cast<int64_t>(window) + sinks;
-  return qsa::paged_splits(T, G, keys);
 }
 
 template <typename P>
@@ -215,8 +209,7 @@ size_t qsa_paged_causal_workspace_size(int64_t T, int H, int G, int page_size, i
                                        int sinks) {
   if (check_heads(T, H, G) != QSA_OK || check_cache(1, 1, page_size, max_pages) != QSA_OK || window < 0 || sinks < 0)
     return 0;
-  const int splits = causal_splits(T, G, page_size, max_pages, window, sinks);
-  return 256 + align256(qsa::paged_partial_bytes(T, G, splits));
+  return 256 + align256(qsa::causal_scratch_bytes());
 }
 
 qsa_status_t qsa_paged_causal(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
@@ -234,10 +227,9 @@ qsa_status_t qsa_paged_causal(const void* q, const void* k_pages, const void* v_
     return QSA_ERR_MISALIGNED;
   if (workspace_bytes < qsa_paged_causal_workspace_size(T, H, G, page_size, max_pages, window, sinks))
     return QSA_ERR_WORKSPACE_TOO_SMALL;
-  const int splits = causal_splits(T, G, page_size, max_pages, window, sinks);
   QSA_TRY(qsa::launch_paged_causal(q, k_pages, v_pages,
                                    view(block_table, kv_len, cu_q, B, n_pages, page_size, max_pages), T, G, window,
-                                   sinks, scale, splits, at<void>(workspace, 256), out, lse,
+                                   sinks, scale, at<int>(workspace, 0), at<void>(workspace, 256), out, lse,
                                    reinterpret_cast<cudaStream_t>(stream)));
   return QSA_OK;
 }

@@ -1,0 +1,960 @@
+// Positional attention of a packed batch's new tokens over a paged K/V cache on
+// the fifth-generation tensor cores: the token at position p sees the keys j <= p
+// with j > p - window or j < sinks (all j <= p without a window).
+//
+// The 12 heads of a KV group read the same keys, so the rows of a query tile are
+// (token, head) pairs: tile i of sequence b and group g holds the flattened rows
+// [128 i, 128 i + 128) of the sequence's 12 n new rows, about 11 tokens, and all of
+// its keys but a few at the diagonal and at the window's edge are seen by every row.
+//
+// Work.  An item (b, i, g) is a run of 128-key tiles.  All tiles of all items, in
+// order, are cut into equal ranges, one per CTA (one CTA per SM), so a decode step
+// over a few long caches and a prompt of many tiles both fill the device; a CTA
+// finds its range by scanning the lengths itself (the host knows none of them).  An
+// item that falls into several ranges leaves unnormalised FP32 sums per range in the
+// workspace, and causal_join_kernel adds them in range order (bit for bit
+// reproducible; at most two parts per CTA).
+//
+// Pipeline of one CTA (12 warps):
+//   warp 8      page lookups and TMA: K as four [128 keys][64 dims] units, V as four
+//               [32 keys][256 dims] units, through one ring of ten 16 KB units in the
+//               order the tensor core consumes them: K0 K1 V0 K2 V1 K3 ...
+//   warp 9      issues S(x) = Q K^T (M 128, N 128) into one of two S buffers, then
+//               O += P V of tile x - 1 (M 128, N 256, P read from tensor memory)
+//   warps 0-7   two softmax warpgroups, even and odd tiles, a thread per row: row
+//               maximum, P = exp2(S scale log2e - m) as BF16 over S's own columns; the
+//               running maximum passes between the groups row by row, and may lag the
+//               true one by 2^8 (P < 256), so O is rescaled only on a jump
+//   warps 10-11 the next item's Q rows (cp.async into the 128-byte swizzle)
+// Tensor memory: O 256 columns, S / P two buffers of 128.
+//
+// Both products cost 1024 tensor cycles per tile (4096 multiply-adds a cycle and SM);
+// the exponentials take 1024 of the MUFU's, under them, so a long chunk is bound by the
+// tensor core and a decode step by the cache's bytes.
+//
+// Values that a row must not see: keys past the diagonal, outside the window, without a
+// page are masked in S.  P V multiplies every V row of the tile, and 0 * NaN is NaN, so in
+// a tile that some row does not see whole, V rows that no row sees are overwritten with
+// zeros, and non-finite elements of rows that only some see are zeroed and added back, in
+// the epilogue, to the rows that see them.
+#include <cuda.h>
+
+#include "qsa_cache.cuh"
+#include "qsa_device.cuh"
+#include "qsa_internal.h"
+
+namespace qsa {
+namespace {
+
+constexpr int kRows = 128;                     // query rows per tile
+constexpr int kTileKeys = 128;
+constexpr int kThreads = 384;
+constexpr int kProducer = 8, kMma = 9, kLoader = 10;  // warps (loader: two)
+constexpr int kUnits = 10;                     // ring units
+constexpr int kUnitBytes = 16384;
+constexpr int kOffRing = kRows * 512;          // Q: four [128][64] blocks, 128-byte swizzle
+constexpr int kOffM = kOffRing + kUnits * kUnitBytes;
+constexpr int kOffL = kOffM + 2 * kRows * 4;
+constexpr int kOffBar = kOffL + kRows * 4;
+// barriers
+constexpr int kBFull = 0, kBEmpty = kBFull + kUnits, kBQFull = kBEmpty + kUnits, kBQEmpty = kBQFull + 1,
+              kBS = kBQEmpty + 1, kBP = kBS + 2, kBM = kBP + 2, kBPv = kBM + 8, kBO = kBPv + 2, kBSync = kBO + 1, kBDrain = kBSync + 1,
+              kBars = kBDrain + 1;
+constexpr int kOffTmem = kOffBar + kBars * 8;
+constexpr int kOffAbort = kOffTmem + 4;
+constexpr int kOffPoison = kOffAbort + 4;      // [2]: the item saw non-finite V it had to take out
+constexpr int kOffStart = kOffPoison + 8;      // the CTA's first tile: sequence, query tile, group, tile
+constexpr int kSmem = kOffStart + 16 + 1024;   // + alignment slack
+static_assert(kSmem <= 232448, "shared memory per block");
+constexpr uint32_t kSpin = 1u << 22;
+constexpr uint32_t kColS = 256;                // tensor-memory columns: O [0, 256), S0, S1
+constexpr float kLag = 8.f;
+constexpr int kMinTiles = 2;                   // fewer tiles than this are not worth a CTA of their own
+constexpr int kMaxCtas = 148;
+constexpr int kPartFloats = kRows * kHeadDim;  // FP32 sums of a part
+// kind::f16, FP32 accumulate, BF16: S (both K-major, N 128) and O (B MN-major, N 256)
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescS = kIdesc | ((128u >> 3) << 17);
+constexpr uint32_t kIdescO = kIdesc | (1u << 16) | ((256u >> 3) << 17);
+
+struct Args {
+  CacheView c;
+  int64_t T;
+  int G;
+  int window, sinks;
+};
+
+// ---------------------------------------------------------------------------
+// items
+// ---------------------------------------------------------------------------
+
+struct Seq {          // one sequence's new tokens (clamped to the packed rows)
+  int start, n;       // packed rows [start, start + n)
+  int64_t p0;         // position of the first
+};
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  Seq s;
+  const int64_t z = min(max(static_cast<int64_t>(__ldg(a.c.cu_q + b + 1)), static_cast<int64_t>(0)), a.T);
+  s.start = static_cast<int>(min(max(static_cast<int64_t>(__ldg(a.c.cu_q + b)), static_cast<int64_t>(0)), z));
+  s.n = static_cast<int>(z - s.start);
+  s.p0 = static_cast<int64_t>(__ldg(a.c.kv_len + b)) - s.n;
+  return s;
+}
+__device__ __forceinline__ int query_tiles(const Seq& s) {
+  return static_cast<int>((static_cast<int64_t>(s.n) * kHeadsPerGroup + kRows - 1) / kRows);
+}
+__device__ __forceinline__ int64_t key_limit(const Args& a) {
+  return static_cast<int64_t>(a.c.max_pages) << a.c.page_shift;
+}
+// Keys [lo, hi) and [0, first) that a token at position p sees.
+__device__ __forceinline__ int row_hi(const Args& a, int64_t p) {
+  return static_cast<int>(max(static_cast<int64_t>(0), min(p + 1, key_limit(a))));
+}
+__device__ __forceinline__ int row_lo(const Args& a, int64_t p) {
+  return a.window > 0 ? static_cast<int>(max(static_cast<int64_t>(0), p + 1 - a.window)) : 0;
+}
+__device__ __forceinline__ int first_keys(const Args& a) { return a.window > 0 ? a.sinks : 0; }
+
+struct Item {         // what query tile i of a sequence sees
+  int rows;           // valid rows
+  int hi0, hi1;       // row_hi of its first and last token
+  int lo0, lo1;       // row_lo of them
+  int n_first;        // key tiles of the first keys in front of the window's
+  int w_first;        // first key tile of the window
+  int n;              // key tiles, at least one
+};
+__device__ __forceinline__ Item item_of(const Args& a, const Seq& s, int i) {
+  Item it;
+  const int64_t r0 = static_cast<int64_t>(i) * kRows, r_end = static_cast<int64_t>(s.n) * kHeadsPerGroup;
+  it.rows = static_cast<int>(min(static_cast<int64_t>(kRows), r_end - r0));
+  const int64_t pa = s.p0 + r0 / kHeadsPerGroup, pz = s.p0 + (r0 + it.rows - 1) / kHeadsPerGroup;
+  it.hi0 = row_hi(a, pa);
+  it.hi1 = row_hi(a, pz);
+  it.lo0 = row_lo(a, pa);
+  it.lo1 = row_lo(a, pz);
+  it.w_first = it.lo0 / kTileKeys;
+  const int first = (min(first_keys(a), it.hi1) + kTileKeys - 1) / kTileKeys;
+  const int n_w = it.hi1 > it.lo0 ? (it.hi1 + kTileKeys - 1) / kTileKeys - it.w_first : 0;
+  if (n_w == 0) it.w_first = 0;
+  it.n_first = n_w > 0 ? min(first, it.w_first) : first;
+  it.n = max(it.n_first + n_w, 1);
+  return it;
+}
+__device__ __forceinline__ int key_tile(const Item& it, int x) {
+  return x < it.n_first ? x : it.w_first + x - it.n_first;
+}
+
+// The CTA's walk: pieces (item, tiles [x0, x1)) of its range.  Every role walks alone.
+struct Walk {
+  int b, i, g, x0, x1;
+  int64_t left;   // tiles after this piece
+  int k;          // piece counter
+  Seq s;
+  Item it;
+  __device__ __forceinline__ void take(const Args& a) {
+    it = item_of(a, s, i);
+    x1 = static_cast<int>(min(static_cast<int64_t>(it.n), x0 + left));
+    left -= x1 - x0;
+  }
+  __device__ __forceinline__ void begin(const Args& a, const int* start, int64_t tiles) {
+    b = start[0], i = start[1], g = start[2], x0 = start[3];
+    left = tiles;
+    k = 0;
+    s = seq_of(a, b);
+    take(a);
+  }
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (left <= 0) return false;
+    ++k;
+    x0 = 0;
+    if (++g == a.G) {
+      g = 0;
+      if (++i == query_tiles(s)) {
+        i = 0;
+        do s = seq_of(a, ++b);
+        while (s.n == 0);
+      }
+    }
+    take(a);
+    return true;
+  }
+};
+
+template <typename V>
+__device__ __forceinline__ V block_scan(V x, V* warp_sums, V& total) {  // inclusive, 384 threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  V before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  return x + before;
+}
+
+// Walks all query tiles in batches of 384, a thread each: f(sequence or -1, query
+// tile, its key tiles times G), called by every thread of the block; stops when it returns true.
+template <class F>
+__device__ __forceinline__ void each_batch(const Args& a, int* pre, long long* sums, F f) {
+  for (int b0 = 0; b0 < a.c.B; b0 += kThreads) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    const int nq = b < a.c.B ? query_tiles(seq_of(a, b)) : 0;
+    int n_all;
+    const int incl = block_scan<int>(nq, reinterpret_cast<int*>(sums), n_all);
+    pre[threadIdx.x] = incl - nq;
+    __syncthreads();
+    for (int j0 = 0; j0 < n_all; j0 += kThreads) {
+      const int j = j0 + static_cast<int>(threadIdx.x);
+      int seq = -1, i = 0;
+      long long w = 0;
+      if (j < n_all) {
+        int lo = 0, hi = kThreads;  // the last sequence of the chunk with pre <= j
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (pre[mid] <= j) lo = mid;
+          else hi = mid;
+        }
+        seq = b0 + lo;
+        i = j - pre[lo];
+        w = static_cast<long long>(item_of(a, seq_of(a, seq), i).n) * a.G;
+      }
+      if (f(seq, i, w)) return;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tensor core, tensor memory, TMA
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {  // 128-byte swizzle, 8-row groups 1024 bytes apart
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ uint64_t desc_v(uint32_t addr) {  // MN-major: 64-dim blocks 4096 bytes apart, 8-key groups 1024
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(4096 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdescS), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(kIdescO), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int row, int chunk, int g, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n" ::"r"(dst),
+      "l"(map), "r"(0), "r"(row), "r"(chunk), "r"(g), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+// Bounded wait that also gives up once another role has.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t it = 0; it < kSpin; ++it) {
+    if (mbar_try(bar, parity)) return true;
+    if ((it & 255) == 255 && *abort_flag) return false;
+  }
+  *abort_flag = 1;
+  return false;
+}
+
+struct Ring {  // position in the ring of units
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == kUnits) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+
+// Part of the workspace per CTA: where its last item goes on.
+struct __align__(16) Cont {
+  int row0;    // packed row of the query tile's first token
+  int rows;    // 0: the CTA's last item ends in its range
+  int first;   // head, within the group, of the query tile's first row
+  int g;
+  int c_last;  // the last CTA with a part
+  int status;  // nonzero: a bounded wait gave up
+  int pad[2];
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+              const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ v_pool, const Args a,
+              float scale_log2, float* __restrict__ part, float2* __restrict__ part_ml, Cont* __restrict__ cont,
+              __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = a.G * kHeadsPerGroup;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffAbort);
+  int* start = reinterpret_cast<int*>(smem + kOffStart);
+  auto bar = [&](int i) { return sb + kOffBar + 8 * i; };
+
+  // ---- the CTA's range of tiles (scratch in the ring, before any copy)
+  int64_t t_begin = 0, t_end = 0, n_tiles = 0;
+  int n_ctas = 1;
+  {
+    int* pre = reinterpret_cast<int*>(smem + kOffRing);
+    long long* sums = reinterpret_cast<long long*>(smem + kOffRing + 4096);
+    long long mine = 0, all = 0;
+    each_batch(a, pre, sums, [&](int, int, long long w) {
+      mine += w;
+      return false;
+    });
+    __syncthreads();
+    block_scan<long long>(mine, sums, all);
+    __syncthreads();
+    n_tiles = all;
+    n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(n_tiles / kMinTiles, static_cast<int64_t>(1))));
+    const int c = static_cast<int>(blockIdx.x);
+    if (tid == 0) cont[c] = Cont{};
+    if (n_tiles == 0 || c >= n_ctas) return;  // uniform
+    t_begin = n_tiles * c / n_ctas;
+    t_end = n_tiles * (c + 1) / n_ctas;
+    long long base = 0;
+    each_batch(a, pre, sums, [&](int seq, int i, long long w) {
+      long long batch;
+      const long long incl = block_scan<long long>(w, sums, batch);
+      const long long at = base + incl - w;
+      if (t_begin >= at && t_begin < at + w) {
+        const int n = static_cast<int>(w / a.G), off = static_cast<int>(t_begin - at);
+        start[0] = seq;
+        start[1] = i;
+        start[2] = off / n;
+        start[3] = off % n;
+      }
+      base += batch;
+      return base > t_begin;
+    });
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(bar(kBFull + i), 1);
+      mbar_init(bar(kBEmpty + i), 1);
+    }
+    mbar_init(bar(kBQFull), 64);
+    mbar_init(bar(kBQEmpty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBS + i), 1);
+      mbar_init(bar(kBP + i), 4);
+      mbar_init(bar(kBPv + i), 1);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(bar(kBM + i), 1);
+    mbar_init(bar(kBO), 8);
+    mbar_init(bar(kBSync), 8);
+    mbar_init(bar(kBDrain), 1);
+    *abort_flag = 0;
+    reinterpret_cast<int*>(smem + kOffPoison)[0] = 0;
+    reinterpret_cast<int*>(smem + kOffPoison)[1] = 0;
+    mbar_fence_init();
+  }
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kOffTmem), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  fence_before();
+  fence_proxy_async();  // the scan's scratch lies where TMA writes next
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
+  const int64_t tiles = t_end - t_begin;
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ K / V units
+    const int page_shift = a.c.page_shift, page = 1 << page_shift;
+    const int n_pg = page < kTileKeys ? kTileKeys >> page_shift : 1;  // pages per tile
+    const int no_row = a.c.n_pages << page_shift;                      // past the pool: TMA fills zeros
+    const int k_box = min(page, kTileKeys);
+    Ring ring;
+    uint32_t issued = 0;
+    bool ok = true;
+    Walk w;
+    w.begin(a, start, tiles);
+    // lane l holds the pool row of the first key of page l of a tile
+    auto rows_of = [&](int x) {
+      const int64_t j = static_cast<int64_t>(key_tile(w.it, x)) * kTileKeys + static_cast<int64_t>(lane) * page;
+      const int r = lane < n_pg ? cache_row(a.c, w.b, j) : -1;
+      return r < 0 ? no_row : r;
+    };
+    auto claim = [&]() {  // the next unit, free and expecting its bytes
+      if (lane == 0) ok = wait_bar(bar(kBEmpty + ring.slot), ring.phase ^ 1, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) return;
+      if (lane == 0) mbar_arrive_tx(bar(kBFull + ring.slot), kUnitBytes);
+      __syncwarp();
+      ++issued;
+    };
+    auto load_k = [&](int rows) {
+      for (int u = 0; u < 4 && ok; ++u) {
+        claim();
+        if (!ok) return;
+        if (lane < n_pg)
+          tma_load(sb + kOffRing + ring.slot * kUnitBytes + lane * k_box * 128, &k_map, rows, u, w.g,
+                   bar(kBFull + ring.slot));
+        ring.step();
+      }
+    };
+    auto load_v = [&](int rows) {
+      for (int u = 0; u < 4 && ok; ++u) {
+        const uint32_t dst = sb + kOffRing + ring.slot * kUnitBytes;
+        if (page >= 32) {
+          const int from = page < kTileKeys ? (32 * u) >> page_shift : 0;
+          int r = __shfl_sync(0xffffffffu, rows, from);
+          r = r == no_row ? no_row : r + 32 * u - (from << page_shift);
+          claim();
+          if (!ok) return;
+          if (lane == 0) tma_load(dst, &v_map, r, 0, w.g, bar(kBFull + ring.slot));
+        } else {  // 16-key pages: lane = half * 4 + 64-dim block
+          const int r = __shfl_sync(0xffffffffu, rows, 2 * u + ((lane >> 2) & 1));
+          claim();
+          if (!ok) return;
+          if (lane < 8)
+            tma_load(dst + (lane & 3) * 4096 + (lane >> 2) * 2048, &v_map, r, lane & 3, w.g, bar(kBFull + ring.slot));
+        }
+        ring.step();
+      }
+    };
+    do {
+      int cur = rows_of(w.x0), prev = 0;
+      for (int x = w.x0; x < w.x1 && ok; ++x) {
+        const int ahead = x + 1 < w.x1 ? rows_of(x + 1) : 0;  // table reads a tile ahead of their use
+        load_k(cur);
+        if (x > w.x0 && ok) load_v(prev);
+        prev = cur;
+        cur = ahead;
+      }
+      if (ok) load_v(prev);
+    } while (ok && w.next(a));
+    if (!ok && lane == 0) {  // copies in flight end before the block does (bounded)
+      Ring r = ring;
+      for (uint32_t i = 0; i < min(issued, static_cast<uint32_t>(kUnits)); ++i) {
+        if (--r.slot < 0) {
+          r.slot = kUnits - 1;
+          r.phase ^= 1;
+        }
+        mbar_wait(bar(kBFull + r.slot), r.phase);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMma) {
+    // ------------------------------------------------------------ tensor core
+    if (lane == 0) {
+      Ring ring;
+      bool ok = true;
+      uint32_t tau = 0;  // tiles so far
+      Walk w;
+      w.begin(a, start, tiles);
+      auto unit = [&]() {
+        ok = ok && wait_bar(bar(kBFull + ring.slot), ring.phase, abort_flag);
+        fence_after();
+        return sb + kOffRing + ring.slot * kUnitBytes;
+      };
+      auto done = [&]() {
+        commit(bar(kBEmpty + ring.slot));
+        ring.step();
+      };
+      auto pv = [&](uint32_t t, bool first) {  // O += P V of tile t
+        const uint32_t b = t & 1;
+        ok = ok && wait_bar(bar(kBP + b), (t >> 1) & 1, abort_flag);
+        if (first && w.k > 0) ok = ok && wait_bar(bar(kBO), (w.k - 1) & 1, abort_flag);
+        const uint32_t p = tmem + kColS + 128 * b;
+        for (int u = 0; u < 4 && ok; ++u) {
+          const uint32_t vb = unit();
+          if (!ok) return;
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+            mma_ts(tmem, p + 8 * (2 * u + kk), desc_v(vb + 2048 * kk), !first || u > 0 || kk > 0);
+          done();
+        }
+        if (ok) commit(bar(kBPv + b));
+      };
+      do {
+        ok = ok && wait_bar(bar(kBQFull), w.k & 1, abort_flag);
+        for (int x = w.x0; x < w.x1 && ok; ++x, ++tau) {
+          const uint32_t s = tmem + kColS + 128 * (tau & 1);
+          for (int u = 0; u < 4 && ok; ++u) {
+            const uint32_t kb = unit();
+            if (!ok) break;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss(s, desc_k_major(sb + u * (kRows * 128) + 32 * kk), desc_k_major(kb + 32 * kk), u > 0 || kk > 0);
+            done();
+          }
+          if (!ok) break;
+          commit(bar(kBS + (tau & 1)));
+          if (x + 1 == w.x1) commit(bar(kBQEmpty));
+          if (x > w.x0) pv(tau - 1, x == w.x0 + 1);
+        }
+        if (ok) pv(tau - 1, w.x1 == w.x0 + 1);
+      } while (ok && w.next(a));
+      if (!ok) {  // the products in flight end before tensor memory is freed (bounded)
+        commit(bar(kBDrain));
+        mbar_wait(bar(kBDrain), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kLoader) {
+    // ------------------------------------------------------------ Q rows
+    Walk w;
+    w.begin(a, start, tiles);
+    bool ok = true;
+    do {
+      if (w.k > 0) ok = wait_bar(bar(kBQEmpty), (w.k - 1) & 1, abort_flag);
+      if (!ok) break;
+      // a warp copies whole 512-byte rows; rows past the last are zeros up to the 32 of a softmax warp
+      const int n = min(kRows, (w.it.rows + 31) & ~31);
+      const int64_t r0 = static_cast<int64_t>(w.i) * kRows;
+      for (int r = warp - kLoader; r < n; r += 2) {
+        const int64_t f = r0 + min(r, w.it.rows - 1);
+        const int64_t t = w.s.start + f / kHeadsPerGroup;
+        const __nv_bfloat16* src =
+            q + (t * H + w.g * kHeadsPerGroup + f % kHeadsPerGroup) * kHeadDim + lane * 8;
+        cp_async16(sb + (lane >> 3) * (kRows * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src, r < w.it.rows);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async();
+      mbar_arrive(bar(kBQFull));
+    } while (w.next(a));
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int wg = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
+    const uint32_t s_addr = tmem + lanes + kColS + 128 * wg;
+    float* sM = reinterpret_cast<float*>(smem + kOffM);
+    float* sL = reinterpret_cast<float*>(smem + kOffL);
+    volatile int* poison = reinterpret_cast<volatile int*>(smem + kOffPoison);
+    const int page_shift = a.c.page_shift;
+    const int n_pg = (1 << page_shift) < kTileKeys ? kTileKeys >> page_shift : 1;
+    const int first = first_keys(a);
+    uint32_t tau = 0, units = 0;  // tiles so far, ring units before the piece
+    bool ok = true;
+    Walk w;
+    w.begin(a, start, tiles);
+    // a barrier of both groups that gives up like every other wait
+    uint32_t syncs = 0;
+    auto both = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBSync));
+      ok = wait_bar(bar(kBSync), syncs++ & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    do {
+      const bool live = 32 * wq < w.it.rows;
+      const int64_t r0 = static_cast<int64_t>(w.i) * kRows;
+      const int64_t p = w.s.p0 + (r0 + row) / kHeadsPerGroup;
+      const int hi = row < w.it.rows ? row_hi(a, p) : 0, lo = row < w.it.rows ? row_lo(a, p) : 0;
+      const int n = w.x1 - w.x0;
+      float m = -INFINITY, l = 0.f;  // this group's running maximum and its part of the row sum
+      for (int y = 0; y < n && ok; ++y, ++tau) {
+        if ((tau & 1) != static_cast<uint32_t>(wg)) continue;
+        const int k0 = key_tile(w.it, w.x0 + y) * kTileKeys;
+        // pages of the tile without a row (read while S is computed)
+        const bool no_page = lane < n_pg && cache_row(a.c, w.b, k0 + (static_cast<int64_t>(lane) << page_shift)) < 0;
+        const uint32_t bad = __ballot_sync(0xffffffffu, no_page);
+        const bool edge = bad != 0 || k0 + kTileKeys > w.it.hi0 || (k0 < w.it.lo1 && k0 + kTileKeys > first);
+        uint32_t vis[4];
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c0 = k0 + 32 * i;
+            vis[i] = low_bits(hi - c0) & (~low_bits(lo - c0) | low_bits(first - c0));
+            if (bad != 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (bad >> (n_pg > 1 ? (32 * i + 16 * h) >> page_shift : 0) & 1) vis[i] &= h ? 0x0000ffffu : 0xffff0000u;
+            }
+          }
+        }
+        ok = wait_bar(bar(kBS + wg), (tau >> 1) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        fence_after();
+        float top = -INFINITY;
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float s[32];
+            tmem_ld32(s_addr + 32 * i, s);
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) top = fmaxf(top, vis[i] >> c & 1 ? s[c] : -INFINITY);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
+            }
+          }
+          top *= scale_log2;
+        }
+        // the running maximum after the tile before, from the other group
+        float m_prev = -INFINITY;
+        if (y > 0) {
+          ok = wait_bar(bar(kBM + 4 * (wg ^ 1) + wq), ((tau - 1) >> 1) & 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          m_prev = sM[(wg ^ 1) * kRows + row];
+        }
+        const float m_new = top > m_prev + kLag ? top : m_prev;
+        sM[wg * kRows + row] = m_new;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBM + 4 * wg + wq));
+        if (live) {
+          // O holds sums against m_prev: rescale the rows whose maximum jumped
+          const bool jump = y > 0 && m_new != m_prev && m_prev != -INFINITY;
+          if (__any_sync(0xffffffffu, jump)) {
+            ok = wait_bar(bar(kBPv + ((tau - 1) & 1)), ((tau - 1) >> 1) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            fence_after();
+            const float f = jump ? exp2_fast(m_prev - m_new) : 1.f;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              float o[32];
+              tmem_ld32(tmem + lanes + 32 * i, o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= f;
+              tmem_st32(tmem + lanes + 32 * i, o);
+            }
+          }
+          if (m_new != m) l *= exp2_fast(m - m_new);
+          m = m_new;
+          const float base = m_new == -INFINITY ? 0.f : m_new;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float s[32];
+            uint32_t pk[16];
+            tmem_ld32(s_addr + 32 * i, s);
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[c] = vis[i] >> c & 1 ? s[c] : -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float p0 = exp2_fast(fmaf(s[c], scale_log2, -base));
+              const float p1 = exp2_fast(fmaf(s[c + 1], scale_log2, -base));
+              l0 += p0;
+              l1 += p1;
+              pk[c >> 1] = pack_bf16(p0, p1);
+            }
+            tmem_st16(s_addr + 16 * i, pk);
+          }
+          l += l0 + l1;
+          tmem_st_wait();
+        }
+        if (edge) {
+          // this thread's key of the tile: V rows that not every query row sees
+          const int j = k0 + row;
+          const bool page_ok = !(bad >> (n_pg > 1 ? row >> page_shift : 0) & 1);
+          const bool any = page_ok && j < w.it.hi1 && (j >= w.it.lo0 || j < first);
+          const bool all = page_ok && j < w.it.hi0 && (j >= w.it.lo1 || j < first);
+          // V of tile y follows K of tile y + 1: units 4 (2 y + 2) on, the last tile's four earlier
+          const uint32_t u = units + (y + 1 < n ? 8 * y + 8 : 8 * y + 4) + (row >> 5);
+          ok = wait_bar(bar(kBFull + u % kUnits), (u / kUnits) & 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t* vr = smem + kOffRing + (u % kUnits) * kUnitBytes + (row & 31) * 128;
+          if (!all) {
+            for (int i = 0; i < 32; ++i) {
+              uint4* x = reinterpret_cast<uint4*>(vr + (i >> 3) * 4096 + (((i & 7) ^ (lane & 7)) << 4));
+              if (!any) {
+                *x = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 val = *x;
+              uint32_t* e = reinterpret_cast<uint32_t*>(&val);
+              bool changed = false;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t z = e[c];
+                if ((z & 0x7f80u) == 0x7f80u) e[c] &= 0xffff0000u;
+                if ((z & 0x7f800000u) == 0x7f800000u) e[c] &= 0x0000ffffu;
+                changed |= e[c] != z;
+              }
+              if (changed) {
+                *x = val;
+                poison[w.k & 1] = 1;
+              }
+            }
+          }
+          fence_proxy_async();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBP + wg));
+      }
+      units += 8 * n;
+      if (!ok) break;
+      // ---- epilogue: the two groups' row sums, then half of the dims each
+      const int last = (tau - 1) & 1;
+      if (!both()) break;  // both groups are past the previous epilogue's reads
+      if (wg != last) sL[row] = l;
+      if (tid == 0) poison[(w.k + 1) & 1] = 0;
+      if (!both()) break;
+      const float m_fin = sM[last * kRows + row];
+      if (wg == last) {
+        const float lo_ = sL[row];
+        if (lo_ != 0.f) l += lo_ * exp2_fast(sM[(wg ^ 1) * kRows + row] - m_fin);
+        sL[row] = l;
+      }
+      const bool poisoned = poison[w.k & 1] != 0;
+      if (!both()) break;
+      const float total = sL[row];
+      ok = wait_bar(bar(kBPv + last), ((tau - 1) >> 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      fence_after();
+      if (live) {
+        const bool whole = w.x0 == 0 && w.x1 == w.it.n;
+        const int64_t f = r0 + row;
+        const int64_t orow = (w.s.start + f / kHeadsPerGroup) * H + w.g * kHeadsPerGroup + f % kHeadsPerGroup;
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (w.x0 == 0 ? 1 : 0);
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll 1
+        for (int i = 4 * wg; i < 4 * wg + 4; ++i) {
+          float o[32];
+          tmem_ld32(tmem + lanes + 32 * i, o);
+          if (poisoned && row < w.it.rows) {
+            // non-finite V elements taken out of the product, back where they are seen
+            const __nv_bfloat16* vp = v_pool + w.g * kHeadDim + 32 * i;
+            auto back = [&](int j) {
+              const int r = cache_row(a.c, w.b, j);
+              if (r < 0) return;
+              for (int c = 0; c < 32; ++c) {
+                const float x = __bfloat162float(vp[static_cast<int64_t>(r) * a.G * kHeadDim + c]);
+#pragma unroll
+                for (int d = 0; d < 32; ++d)
+                  if (d == c && !isfinite(x)) o[d] += x;
+              }
+            };
+            for (int j = w.it.hi0; j < hi; ++j)
+              if (j >= lo || j < first) back(j);
+            for (int j = max(lo, w.it.lo0); j < min(w.it.lo1, min(hi, w.it.hi0)); ++j)
+              if (j >= first) back(j);
+          }
+          if (row < w.it.rows) {
+            if (whole) {
+              uint4* y = reinterpret_cast<uint4*>(out + orow * kHeadDim + 32 * i);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                y[c] = make_uint4(pack_bf16(o[8 * c] * inv, o[8 * c + 1] * inv),
+                                  pack_bf16(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
+                                  pack_bf16(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
+                                  pack_bf16(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+            } else {
+              float4* y = reinterpret_cast<float4*>(part + static_cast<int64_t>(slot) * kPartFloats + row * kHeadDim +
+                                                    32 * i);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) y[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            }
+          }
+          __syncwarp();
+        }
+        if (wg == last && row < w.it.rows) {
+          if (whole) lse[orow] = total == 0.f ? -INFINITY : (m_fin + log2f(total)) * kLn2;
+          else part_ml[slot * kRows + row] = make_float2(m_fin, total);
+        }
+      }
+      if (tid == 0 && w.x0 == 0 && w.x1 < w.it.n) {  // the item goes on in the ranges behind this one
+        Cont ct{};
+        ct.row0 = w.s.start + static_cast<int>(r0 / kHeadsPerGroup);
+        ct.first = static_cast<int>(r0 % kHeadsPerGroup);
+        ct.rows = w.it.rows;
+        ct.g = w.g;
+        const int64_t item_end = t_end - (w.x1 - w.x0) + w.it.n;  // this piece is the range's last
+        ct.c_last = static_cast<int>((item_end * n_ctas - 1) / n_tiles);
+        cont[blockIdx.x] = ct;
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBO));
+    } while (w.next(a));
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512));
+  if (tid == 0 && *abort_flag) cont[blockIdx.x].status = 2;
+}
+
+// Joins the parts of the item that CTA range blockIdx.x begins and does not
+// end: block row y takes the item's rows y, y + gridDim.y, ..., its eight
+// warps an eighth of the parts each, added in order.  Also gathers the ranges'
+// status into the call's.
+constexpr int kJoinWarps = 8, kJoinRows = 16;
+__global__ void __launch_bounds__(kJoinWarps * 32)
+causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ part_ml, const Cont* __restrict__ cont,
+                   int G, int* __restrict__ status, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  __shared__ float sO[kJoinWarps][kHeadDim];
+  __shared__ float sL[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int bad = 0;
+    for (int c = threadIdx.x; c < static_cast<int>(gridDim.x); c += blockDim.x) bad |= cont[c].status;
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *status = bad ? 2 : 0;
+  }
+  const Cont ct = cont[c0];
+  const int n = ct.c_last - c0 + 1;  // part 0: slot (c0, 1), part i: slot (c0 + i, 0)
+  auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
+  for (int r = blockIdx.y; r < ct.rows; r += gridDim.y) {
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part_ml[slot(i) * kRows + r].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    float l = 0.f, o[8] = {};
+#pragma unroll 4
+    for (int i = n * warp / kJoinWarps; i < n * (warp + 1) / kJoinWarps; ++i) {
+      const float2 ml = part_ml[slot(i) * kRows + r];
+      const float4* p = reinterpret_cast<const float4*>(part + static_cast<int64_t>(slot(i)) * kPartFloats + r * kHeadDim) +
+                        2 * lane;
+      const float4 u = p[0], v = p[1];
+      const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - m);  // sums without a maximum are zeros or NaN
+      l += ml.y * f;
+      o[0] += u.x * f, o[1] += u.y * f, o[2] += u.z * f, o[3] += u.w * f;
+      o[4] += v.x * f, o[5] += v.y * f, o[6] += v.z * f, o[7] += v.w * f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sO[warp][8 * lane + i] = o[i];
+    if (lane == 0) sL[warp] = l;
+    __syncthreads();
+    float total = 0.f, y = 0.f;
+#pragma unroll
+    for (int x = 0; x < kJoinWarps; ++x) {
+      total += sL[x];
+      y += sO[x][threadIdx.x];
+    }
+    const int f = ct.first + r;
+    const int64_t orow = (static_cast<int64_t>(ct.row0) + f / kHeadsPerGroup) * G * kHeadsPerGroup +
+                         ct.g * kHeadsPerGroup + f % kHeadsPerGroup;
+    out[orow * kHeadDim + threadIdx.x] = __float2bfloat16_rn(total == 0.f ? 0.f : y / total);
+    if (threadIdx.x == 0) lse[orow] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
+  }
+}
+
+// The pool as {64 dims, rows, four 64-dim blocks, G}: a box is rows of one page, swizzled.
+bool encode_pool(CUtensorMap* map, const void* pool, uint64_t rows, int G, uint32_t box_rows, uint32_t box_blocks) {
+  const auto fn = reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                                CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                                CUtensorMapFloatOOBfill)>(tensor_map_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, rows, 4, static_cast<cuuint64_t>(G)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(G) * 512, 128, 512};
+  cuuint32_t box[4] = {64, box_rows, box_blocks, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kContBytes = (kMaxCtas * sizeof(Cont) + 255) / 256 * 256;
+constexpr size_t kMlBytes = 2 * kMaxCtas * kRows * sizeof(float2);
+
+}  // namespace
+
+size_t causal_scratch_bytes() { return kContBytes + kMlBytes + 2 * kMaxCtas * static_cast<size_t>(kPartFloats) * 4; }
+
+cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* v_pages, const CacheView& c, int64_t T,
+                                int G, int window, int sinks, float scale, int* status, void* scratch, void* out,
+                                float* lse, cudaStream_t s) {
+  CUtensorMap k_map, v_map;
+  const uint32_t page = 1u << c.page_shift;
+  const uint64_t rows = static_cast<uint64_t>(c.n_pages) << c.page_shift;
+  if (!encode_pool(&k_map, k_pages, rows, G, page < kTileKeys ? page : kTileKeys, 1) ||
+      !encode_pool(&v_map, v_pages, rows, G, page < 32 ? page : 32, page < 32 ? 1 : 4))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(causal_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  uint8_t* ws = static_cast<uint8_t*>(scratch);
+  Cont* cont = reinterpret_cast<Cont*>(ws);
+  float2* ml = reinterpret_cast<float2*>(ws + kContBytes);
+  float* part = reinterpret_cast<float*>(ws + kContBytes + kMlBytes);
+  const int grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+  causal_kernel<<<grid, kThreads, kSmem, s>>>(k_map, v_map, static_cast<const __nv_bfloat16*>(q),
+                                              static_cast<const __nv_bfloat16*>(v_pages), Args{c, T, G, window, sinks},
+                                              scale * kLog2e, part, ml, cont, static_cast<__nv_bfloat16*>(out), lse);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  causal_join_kernel<<<dim3(grid, kJoinRows), kJoinWarps * 32, 0, s>>>(part, ml, cont, G, status,
+                                                                      static_cast<__nv_bfloat16*>(out), lse);
+  return cudaGetLastError();
+}
+
+}  // namespace qsa

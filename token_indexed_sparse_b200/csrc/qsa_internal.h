@@ -141,9 +141,14 @@ size_t paged_partial_bytes(int64_t T, int G, int splits);
 cudaError_t launch_paged_forward(const void* q, const void* k_pages, const void* v_pages, const CacheView& c,
                                  const int32_t* row_cnt, const int32_t* row_cols, int64_t T, int G, int n_sel,
                                  float scale, int splits, void* partial, void* out, float* lse, cudaStream_t s);
-// The same over the keys j <= position with j > position - window (when window > 0) or j < sinks.
+// Attention of a packed batch's new tokens over the keys j <= position with j > position - window
+// (when window > 0) or j < sinks (qsa_causal.cu).  `scratch`: causal_scratch_bytes, 256-byte aligned;
+// *status is set to 2 if a bounded wait gave up, else 0.
+size_t causal_scratch_bytes();
 cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* v_pages, const CacheView& c, int64_t T,
-                                int G, int window, int sinks, float scale, int splits, void* partial, void* out,
+                                int G, int window, int sinks, float scale, int* status, void* scratch, void* out,
                                 float* lse, cudaStream_t s);
+// The driver's cuTensorMapEncodeTiled, or null (qsa_selector.cu).
+void* tensor_map_encoder();
 
 }  // namespace qsa

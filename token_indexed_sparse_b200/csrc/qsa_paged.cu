@@ -50,9 +50,6 @@ struct RouteKeys {
   const int32_t* row_cols;
   int n_sel;
 };
-struct RangeKeys {
-  int window, sinks;
-};
 struct Keys {  // the keys of one row: key i is cols[i], or i < n_first ? i : base + i
   const int32_t* cols;
   int64_t base;
@@ -68,19 +65,6 @@ __device__ __forceinline__ Keys row_keys(const RouteKeys& r, const CacheView& c,
   k.limit = __ldg(c.kv_len + seq);
   return k;
 }
-__device__ __forceinline__ Keys row_keys(const RangeKeys& r, const CacheView& c, int seq, int64_t t) {
-  const int64_t p = cache_pos(c, seq, t);
-  const int64_t hi = min(p + 1, static_cast<int64_t>(c.max_pages) << c.page_shift);
-  const int64_t lo = r.window > 0 ? max(static_cast<int64_t>(0), p + 1 - r.window) : 0;
-  Keys k;
-  k.cols = nullptr;
-  k.n_first = static_cast<int>(max(static_cast<int64_t>(0), min(min(static_cast<int64_t>(r.sinks), lo), hi)));
-  k.base = lo - k.n_first;
-  k.cnt = static_cast<int>(k.n_first + max(static_cast<int64_t>(0), hi - lo));
-  k.limit = hi;
-  return k;
-}
-
 template <class Source>
 __global__ void __launch_bounds__(kThreads, kCps)
 paged_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
@@ -446,12 +430,6 @@ cudaError_t launch_paged_forward(const void* q, const void* k_pages, const void*
                                  const int32_t* row_cnt, const int32_t* row_cols, int64_t T, int G, int n_sel,
                                  float scale, int splits, void* partial, void* out, float* lse, cudaStream_t s) {
   return launch(q, k_pages, v_pages, c, RouteKeys{row_cnt, row_cols, n_sel}, T, G, scale, splits, partial, out, lse, s);
-}
-
-cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* v_pages, const CacheView& c, int64_t T,
-                                int G, int window, int sinks, float scale, int splits, void* partial, void* out,
-                                float* lse, cudaStream_t s) {
-  return launch(q, k_pages, v_pages, c, RangeKeys{window, sinks}, T, G, scale, splits, partial, out, lse, s);
 }
 
 }  // namespace qsa

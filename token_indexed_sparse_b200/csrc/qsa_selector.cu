@@ -402,6 +402,8 @@ bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box
 
 }  // namespace
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+
 cudaError_t launch_selector_scores(const void* qi, const void* kbar, int64_t T, int64_t NB, int Hi, float scale,
                                    const int32_t* pos, const int32_t* blk_base, const int32_t* tok_base,
                                    float* scores, int64_t stride, int* status, cudaStream_t s) {
