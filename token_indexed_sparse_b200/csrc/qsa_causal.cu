@@ -16,16 +16,15 @@
 // reproducible; at most two parts per CTA).
 //
 // Pipeline of one CTA (12 warps):
-//   warp 8      page lookups and TMA: K as four [128 keys][64 dims] units, V as four
-//               [32 keys][256 dims] units, through one ring of ten 16 KB units in the
-//               order the tensor core consumes them: K0 K1 V0 K2 V1 K3 ...
-//   warp 9      issues S(x) = Q K^T (M 128, N 128) into one of two S buffers, then
-//               O += P V of tile x - 1 (M 128, N 256, P read from tensor memory)
-//   warps 0-7   two softmax warpgroups, even and odd tiles, a thread per row: row
-//               maximum, P = exp2(S scale log2e - m) as BF16 over S's own columns; the
-//               running maximum passes between the groups row by row, and may lag the
-//               true one by 2^8 (P < 256), so O is rescaled only on a jump
-//   warps 10-11 the next item's Q rows (cp.async into the 128-byte swizzle)
+//   warp 8      page lookups and TMA: K as two [128 keys][128 dims] units, V as two
+//               [64 keys][256 dims] units, through one ring of five 32 KB units in the order
+//               the tensor core consumes them: K0 K1 V0 K2 V1 K3 ...
+//   warp 9      issues S(x) = Q K^T (M 128, N 128) into one of two S buffers
+//   warp 10     issues O += P V (M 128, N 256, P read from tensor memory)
+//   warps 0-7   softmax: row r of the tile on two threads, 64 keys each: P = exp2(S scale
+//               log2e - m) as BF16 over the half's own S columns; the running maximum m may
+//               lag the true one by 2^8 (P < 256), so O is rescaled only on a jump
+//   warp 11     the next item's Q rows (cp.async into the 128-byte swizzle)
 // Tensor memory: O 256 columns, S / P two buffers of 128.
 //
 // Both products cost 1024 tensor cycles per tile (4096 multiply-adds a cycle and SM);
@@ -49,24 +48,24 @@ namespace {
 constexpr int kRows = 128;                     // query rows per tile
 constexpr int kTileKeys = 128;
 constexpr int kThreads = 384;
-constexpr int kProducer = 8, kMma = 9, kLoader = 10;  // warps (loader: two)
-constexpr int kUnits = 10;                     // ring units
-constexpr int kUnitBytes = 16384;
+constexpr int kProducer = 8, kMmaS = 9, kMmaO = 10, kLoader = 11;  // warps
+constexpr int kUnits = 5;                      // ring units
+constexpr int kSubBytes = 16384;               // K: [128 keys][64 dims]; V: [32 keys][256 dims]
+constexpr int kUnitBytes = 2 * kSubBytes;
 constexpr int kOffRing = kRows * 512;          // Q: four [128][64] blocks, 128-byte swizzle
-constexpr int kOffM = kOffRing + kUnits * kUnitBytes;
-constexpr int kOffL = kOffM + 2 * kRows * 4;
-constexpr int kOffBar = kOffL + kRows * 4;
+constexpr int kOffX = kOffRing + kUnits * kUnitBytes;  // [2][2][128] floats that a row's threads exchange
+constexpr int kOffBar = kOffX + 4 * kRows * 4;
 // barriers
 constexpr int kBFull = 0, kBEmpty = kBFull + kUnits, kBQFull = kBEmpty + kUnits, kBQEmpty = kBQFull + 1,
-              kBS = kBQEmpty + 1, kBP = kBS + 2, kBM = kBP + 2, kBPv = kBM + 8, kBO = kBPv + 2, kBSync = kBO + 1, kBDrain = kBSync + 1,
-              kBars = kBDrain + 1;
+              kBS = kBQEmpty + 1, kBP = kBS + 2, kBPv = kBP + 2, kBO = kBPv + 2, kBDrain = kBO + 1,
+              kBars = kBDrain + 2;
 constexpr int kOffTmem = kOffBar + kBars * 8;
 constexpr int kOffAbort = kOffTmem + 4;
-constexpr int kOffPoison = kOffAbort + 4;      // [2]: the item saw non-finite V it had to take out
-constexpr int kOffStart = kOffPoison + 8;      // the CTA's first tile: sequence, query tile, group, tile
-constexpr int kSmem = kOffStart + 16 + 1024;   // + alignment slack
+constexpr int kOffPoison = kOffAbort + 4;      // [3]: the item saw non-finite V it had to take out
+constexpr int kOffStart = kOffPoison + 12;     // the CTA's first tile: sequence, query tile, group, tile
+constexpr int kSmem = kOffStart + 16;          // no room to align the base: checked instead
 static_assert(kSmem <= 232448, "shared memory per block");
-constexpr uint32_t kSpin = 1u << 22;
+constexpr uint32_t kSpin = 1u << 26;           // polls before a wait gives up (seconds)
 constexpr uint32_t kColS = 256;                // tensor-memory columns: O [0, 256), S0, S1
 constexpr float kLag = 8.f;
 constexpr int kMinTiles = 2;                   // fewer tiles than this are not worth a CTA of their own
@@ -278,6 +277,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -288,12 +306,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
       "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -313,22 +333,43 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
-// Bounded wait that also gives up once another role has.
+// Bounded wait that also gives up once another role has.  It polls with test_wait: a thread that
+// try_wait has put to sleep for some thousands of cycles wakes up to a thousand late, which
+// every tile would pay several times over.
+__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  for (uint32_t it = 0; it < kSpin; ++it) {
-    if (mbar_try(bar, parity)) return true;
-    if ((it & 255) == 255 && *abort_flag) return false;
+  bool ok = test_bar(bar, parity);
+#pragma unroll 1
+  for (uint32_t it = 0; !ok && it < kSpin; ++it) {
+    ok = test_bar(bar, parity);
+    if ((it & 255) == 255 && *abort_flag) break;
   }
-  *abort_flag = 1;
-  return false;
+  if (!ok) *abort_flag = 1;
+  return ok;
+}
+// Brings a warp's lanes together without __syncwarp's memory ordering, which waits for every read
+// in flight (a page of the block table: 800 cycles).
+__device__ __forceinline__ void converge() {
+  asm volatile("{\n .reg .pred p, q;\n setp.eq.u32 q, 0, 0;\n vote.sync.all.pred p, q, 0xffffffff;\n}\n");
+}
+// The same for a whole warp: every lane polls (and so has the barrier's ordering itself), all agree.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
 }
 
 struct Ring {  // position in the ring of units
   int slot = 0;
   uint32_t phase = 0;
-  __device__ __forceinline__ void step() {
-    if (++slot == kUnits) {
-      slot = 0;
+  __device__ __forceinline__ void step(int n = 1) {  // n <= kUnits
+    slot += n;
+    if (slot >= kUnits) {
+      slot -= kUnits;
       phase ^= 1;
     }
   }
@@ -354,8 +395,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ v_pool, const Args a,
               float scale_log2, float* __restrict__ part, float2* __restrict__ part_ml, Cont* __restrict__ cont,
               __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.G * kHeadsPerGroup;
@@ -380,8 +420,13 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     n_tiles = all;
     n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(n_tiles / kMinTiles, static_cast<int64_t>(1))));
     const int c = static_cast<int>(blockIdx.x);
-    if (tid == 0) cont[c] = Cont{};
-    if (n_tiles == 0 || c >= n_ctas) return;  // uniform
+    const bool aligned = (sb & 1023) == 0;  // what the 128-byte swizzle needs
+    if (tid == 0) {
+      Cont ct{};
+      ct.status = aligned ? 0 : 2;
+      cont[c] = ct;
+    }
+    if (n_tiles == 0 || c >= n_ctas || !aligned) return;  // uniform
     t_begin = n_tiles * c / n_ctas;
     t_end = n_tiles * (c + 1) / n_ctas;
     long long base = 0;
@@ -405,23 +450,21 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       mbar_init(bar(kBFull + i), 1);
       mbar_init(bar(kBEmpty + i), 1);
     }
-    mbar_init(bar(kBQFull), 64);
+    mbar_init(bar(kBQFull), 32);
     mbar_init(bar(kBQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBS + i), 1);
-      mbar_init(bar(kBP + i), 4);
+      mbar_init(bar(kBP + i), 8);
       mbar_init(bar(kBPv + i), 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(bar(kBM + i), 1);
     mbar_init(bar(kBO), 8);
-    mbar_init(bar(kBSync), 8);
     mbar_init(bar(kBDrain), 1);
+    mbar_init(bar(kBDrain + 1), 1);
     *abort_flag = 0;
-    reinterpret_cast<int*>(smem + kOffPoison)[0] = 0;
-    reinterpret_cast<int*>(smem + kOffPoison)[1] = 0;
+    for (int i = 0; i < 3; ++i) reinterpret_cast<int*>(smem + kOffPoison)[i] = 0;
     mbar_fence_init();
   }
-  if (warp == kMma) {
+  if (warp == kMmaS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kOffTmem), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
@@ -450,39 +493,43 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       return r < 0 ? no_row : r;
     };
     auto claim = [&]() {  // the next unit, free and expecting its bytes
-      if (lane == 0) ok = wait_bar(bar(kBEmpty + ring.slot), ring.phase ^ 1, abort_flag);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = warp_wait(bar(kBEmpty + ring.slot), ring.phase ^ 1, abort_flag);
       if (!ok) return;
       if (lane == 0) mbar_arrive_tx(bar(kBFull + ring.slot), kUnitBytes);
       __syncwarp();
       ++issued;
     };
     auto load_k = [&](int rows) {
-      for (int u = 0; u < 4 && ok; ++u) {
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
         claim();
         if (!ok) return;
-        if (lane < n_pg)
-          tma_load(sb + kOffRing + ring.slot * kUnitBytes + lane * k_box * 128, &k_map, rows, u, w.g,
-                   bar(kBFull + ring.slot));
+        // lane = block of 64 dims * pages + page
+        const int blk = lane >= n_pg ? 1 : 0, pg = lane - blk * n_pg;
+        const int r = __shfl_sync(0xffffffffu, rows, pg & 31);
+        if (lane < 2 * n_pg)
+          tma_load(sb + kOffRing + ring.slot * kUnitBytes + blk * kSubBytes + pg * k_box * 128, &k_map, r, 2 * u + blk,
+                   w.g, bar(kBFull + ring.slot));
         ring.step();
       }
     };
     auto load_v = [&](int rows) {
-      for (int u = 0; u < 4 && ok; ++u) {
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        claim();
+        if (!ok) return;
         const uint32_t dst = sb + kOffRing + ring.slot * kUnitBytes;
-        if (page >= 32) {
-          const int from = page < kTileKeys ? (32 * u) >> page_shift : 0;
-          int r = __shfl_sync(0xffffffffu, rows, from);
-          r = r == no_row ? no_row : r + 32 * u - (from << page_shift);
-          claim();
-          if (!ok) return;
-          if (lane == 0) tma_load(dst, &v_map, r, 0, w.g, bar(kBFull + ring.slot));
-        } else {  // 16-key pages: lane = half * 4 + 64-dim block
-          const int r = __shfl_sync(0xffffffffu, rows, 2 * u + ((lane >> 2) & 1));
-          claim();
-          if (!ok) return;
-          if (lane < 8)
-            tma_load(dst + (lane & 3) * 4096 + (lane >> 2) * 2048, &v_map, r, lane & 3, w.g, bar(kBFull + ring.slot));
+        if (page >= 32) {  // lane = run of 32 keys
+          const int key = 64 * u + 32 * (lane & 1), from = page < kTileKeys ? key >> page_shift : 0;
+          const int r = __shfl_sync(0xffffffffu, rows, from);
+          if (lane < 2)
+            tma_load(dst + lane * kSubBytes, &v_map, r == no_row ? no_row : r + key - (from << page_shift), 0, w.g,
+                     bar(kBFull + ring.slot));
+        } else {  // 16-key pages: lane = page * 4 + block of 64 dims
+          const int r = __shfl_sync(0xffffffffu, rows, 4 * u + ((lane >> 2) & 3));
+          if (lane < 16)
+            tma_load(dst + (lane >> 3) * kSubBytes + ((lane >> 2) & 1) * 2048 + (lane & 3) * 4096, &v_map, r, lane & 3,
+                     w.g, bar(kBFull + ring.slot));
         }
         ring.step();
       }
@@ -509,60 +556,80 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       }
     }
     __syncwarp();
-  } else if (warp == kMma) {
+  } else if (warp == kMmaS || warp == kMmaO) {
     // ------------------------------------------------------------ tensor core
+    // One thread per product: each wait and commit stalls its thread for longer than the few
+    // instructions that queue at the tensor core last, so one thread alone left it idle for
+    // half of the time; two keep it fed.
     if (lane == 0) {
       Ring ring;
       bool ok = true;
       uint32_t tau = 0;  // tiles so far
       Walk w;
       w.begin(a, start, tiles);
-      auto unit = [&]() {
-        ok = ok && wait_bar(bar(kBFull + ring.slot), ring.phase, abort_flag);
-        fence_after();
-        return sb + kOffRing + ring.slot * kUnitBytes;
-      };
-      auto done = [&]() {
-        commit(bar(kBEmpty + ring.slot));
-        ring.step();
-      };
-      auto pv = [&](uint32_t t, bool first) {  // O += P V of tile t
-        const uint32_t b = t & 1;
-        ok = ok && wait_bar(bar(kBP + b), (t >> 1) & 1, abort_flag);
-        if (first && w.k > 0) ok = ok && wait_bar(bar(kBO), (w.k - 1) & 1, abort_flag);
-        const uint32_t p = tmem + kColS + 128 * b;
-        for (int u = 0; u < 4 && ok; ++u) {
-          const uint32_t vb = unit();
-          if (!ok) return;
+      auto wait = [&](int i, uint32_t parity) { return wait_bar(bar(i), parity, abort_flag); };
+      if (warp == kMmaS) {
+        const uint64_t q_desc = desc_k_major(sb), k_desc = desc_k_major(sb + kOffRing);
+        do {
+          ok = wait(kBQFull, w.k & 1);
+          const int n = w.x1 - w.x0;
+#pragma unroll 1
+          for (int y = 0; y < n && ok; ++y, ++tau) {
+            const uint32_t s = tmem + kColS + 128 * (tau & 1);
+            if (tau >= 2) ok = wait(kBPv + (tau & 1), ((tau - 2) >> 1) & 1);  // P of tile tau - 2 has been read
+#pragma unroll 1
+            for (int u = 0; u < 2 && ok; ++u) {
+              ok = wait(kBFull + ring.slot, ring.phase);
+              if (!ok) break;
+              fence_after();
+              const uint64_t kd = k_desc + ring.slot * (kUnitBytes >> 4), qd = q_desc + u * (2 * kRows * 128 >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            mma_ts(tmem, p + 8 * (2 * u + kk), desc_v(vb + 2048 * kk), !first || u > 0 || kk > 0);
-          done();
-        }
-        if (ok) commit(bar(kBPv + b));
-      };
-      do {
-        ok = ok && wait_bar(bar(kBQFull), w.k & 1, abort_flag);
-        for (int x = w.x0; x < w.x1 && ok; ++x, ++tau) {
-          const uint32_t s = tmem + kColS + 128 * (tau & 1);
-          for (int u = 0; u < 4 && ok; ++u) {
-            const uint32_t kb = unit();
+              for (int i = 0; i < 8; ++i)
+                mma_ss(s, qd + (i >> 2) * (kRows * 128 >> 4) + 2 * (i & 3), kd + (i >> 2) * (kSubBytes >> 4) + 2 * (i & 3),
+                       i > 0 || u > 0);
+              commit(bar(kBEmpty + ring.slot));
+              ring.step();
+            }
             if (!ok) break;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss(s, desc_k_major(sb + u * (kRows * 128) + 32 * kk), desc_k_major(kb + 32 * kk), u > 0 || kk > 0);
-            done();
+            commit(bar(kBS + (tau & 1)));
+            if (y > 0) ring.step(2);  // V of tile y - 1
           }
-          if (!ok) break;
-          commit(bar(kBS + (tau & 1)));
-          if (x + 1 == w.x1) commit(bar(kBQEmpty));
-          if (x > w.x0) pv(tau - 1, x == w.x0 + 1);
-        }
-        if (ok) pv(tau - 1, w.x1 == w.x0 + 1);
-      } while (ok && w.next(a));
+          if (ok) commit(bar(kBQEmpty));
+          ring.step(2);               // V of the last tile
+        } while (ok && w.next(a));
+      } else {
+        const uint64_t v_desc = desc_v(sb + kOffRing);
+        do {
+          const int n = w.x1 - w.x0;
+          ring.step(n > 1 ? 4 : 2);   // K of the first two tiles
+#pragma unroll 1
+          for (int y = 0; y < n && ok; ++y, ++tau) {
+            const uint32_t p = tmem + kColS + 128 * (tau & 1);
+            ok = wait(kBP + (tau & 1), (tau >> 1) & 1);
+            if (ok && y == 0 && w.k > 0) ok = wait(kBO, (w.k - 1) & 1);  // the sums before have been read
+#pragma unroll 1
+            for (int u = 0; u < 2 && ok; ++u) {
+              ok = wait(kBFull + ring.slot, ring.phase);
+              if (!ok) break;
+              fence_after();
+              const uint64_t vd = v_desc + ring.slot * (kUnitBytes >> 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_ts(tmem, p + 64 * u + 8 * i, vd + (i >> 1) * (kSubBytes >> 4) + (i & 1) * (2048 >> 4),
+                       y > 0 || u > 0 || i > 0);
+              commit(bar(kBEmpty + ring.slot));
+              ring.step();
+            }
+            if (!ok) break;
+            commit(bar(kBPv + (tau & 1)));
+            if (y + 2 < n) ring.step(2);  // K of tile y + 2
+          }
+        } while (ok && w.next(a));
+      }
       if (!ok) {  // the products in flight end before tensor memory is freed (bounded)
-        commit(bar(kBDrain));
-        mbar_wait(bar(kBDrain), 0);
+        const int i = kBDrain + (warp == kMmaO ? 1 : 0);
+        commit(bar(i));
+        mbar_wait(bar(i), 0);
       }
     }
     __syncwarp();
@@ -572,12 +639,12 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     w.begin(a, start, tiles);
     bool ok = true;
     do {
-      if (w.k > 0) ok = wait_bar(bar(kBQEmpty), (w.k - 1) & 1, abort_flag);
+      if (w.k > 0) ok = warp_wait(bar(kBQEmpty), (w.k - 1) & 1, abort_flag);
       if (!ok) break;
       // a warp copies whole 512-byte rows; rows past the last are zeros up to the 32 of a softmax warp
       const int n = min(kRows, (w.it.rows + 31) & ~31);
       const int64_t r0 = static_cast<int64_t>(w.i) * kRows;
-      for (int r = warp - kLoader; r < n; r += 2) {
+      for (int r = 0; r < n; ++r) {
         const int64_t f = r0 + min(r, w.it.rows - 1);
         const int64_t t = w.s.start + f / kHeadsPerGroup;
         const __nv_bfloat16* src =
@@ -591,145 +658,136 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     } while (w.next(a));
   } else {
     // ------------------------------------------------------------ softmax
-    const int wg = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
-    const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
-    const uint32_t s_addr = tmem + lanes + kColS + 128 * wg;
-    float* sM = reinterpret_cast<float*>(smem + kOffM);
-    float* sL = reinterpret_cast<float*>(smem + kOffL);
+    // Thread (half, row): keys 64 half .. 64 half + 63 of every tile.  Both halves of a tile at once
+    // (against a tile per warpgroup, two at a time) halve the time between S and P, which is
+    // what keeps the tensor core waiting.  A wait that gives up does not end the walk: every wait
+    // after it returns at once, so the hardware barriers below always meet.
+    const int half = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
+    volatile float* sX = reinterpret_cast<volatile float*>(smem + kOffX);
     volatile int* poison = reinterpret_cast<volatile int*>(smem + kOffPoison);
     const int page_shift = a.c.page_shift;
     const int n_pg = (1 << page_shift) < kTileKeys ? kTileKeys >> page_shift : 1;
     const int first = first_keys(a);
     uint32_t tau = 0, units = 0;  // tiles so far, ring units before the piece
-    bool ok = true;
+    uint32_t ex = 0;              // exchanges so far
+    auto wait = [&](int i, uint32_t parity) {
+      wait_bar(bar(i), parity, abort_flag);
+      converge();
+    };
+    // the other thread's value of the row (two buffers in turn: a buffer is written again only after
+    // the exchange behind it, which both have reached)
+    auto other = [&](float x) {
+      volatile float* buf = sX + (ex++ & 1) * 2 * kRows;
+      buf[half * kRows + row] = x;
+      bar_sync(1 + wq, 64);
+      return buf[(half ^ 1) * kRows + row];
+    };
     Walk w;
     w.begin(a, start, tiles);
-    // a barrier of both groups that gives up like every other wait
-    uint32_t syncs = 0;
-    auto both = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBSync));
-      ok = wait_bar(bar(kBSync), syncs++ & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      return ok;
-    };
     do {
       const bool live = 32 * wq < w.it.rows;
       const int64_t r0 = static_cast<int64_t>(w.i) * kRows;
       const int64_t p = w.s.p0 + (r0 + row) / kHeadsPerGroup;
       const int hi = row < w.it.rows ? row_hi(a, p) : 0, lo = row < w.it.rows ? row_lo(a, p) : 0;
       const int n = w.x1 - w.x0;
-      float m = -INFINITY, l = 0.f;  // this group's running maximum and its part of the row sum
-      for (int y = 0; y < n && ok; ++y, ++tau) {
-        if ((tau & 1) != static_cast<uint32_t>(wg)) continue;
+      // Lane l's page of the l-th page of tile y, read a tile ahead of its use
+      // (volatile: sunk to its use, the read's latency stood between S and P of every tile).
+      auto page_of = [&](int y) {
+        if (y >= n || lane >= n_pg) return -1;
+        const int64_t pg = (static_cast<int64_t>(key_tile(w.it, w.x0 + y)) * kTileKeys >> page_shift) + lane;
+        if (pg >= a.c.max_pages) return -1;
+        int v;
+        asm volatile("ld.global.nc.b32 %0, [%1];\n"
+                     : "=r"(v) : "l"(a.c.table + static_cast<int64_t>(w.b) * a.c.max_pages + pg));
+        return v;
+      };
+      int page = page_of(0);
+      float m = -INFINITY, l = 0.f;  // the row's running maximum; this half's part of its sum
+      for (int y = 0; y < n; ++y, ++tau) {
         const int k0 = key_tile(w.it, w.x0 + y) * kTileKeys;
-        // pages of the tile without a row (read while S is computed)
-        const bool no_page = lane < n_pg && cache_row(a.c, w.b, k0 + (static_cast<int64_t>(lane) << page_shift)) < 0;
-        const uint32_t bad = __ballot_sync(0xffffffffu, no_page);
+        // pages of the tile without a row
+        const uint32_t bad = __ballot_sync(0xffffffffu, lane < n_pg && (page < 0 || page >= a.c.n_pages));
+        page = page_of(y + 1);
         const bool edge = bad != 0 || k0 + kTileKeys > w.it.hi0 || (k0 < w.it.lo1 && k0 + kTileKeys > first);
-        uint32_t vis[4];
-        if (edge) {
+        // the row's visible keys among 32 i .. 32 i + 31 of the tile
+        auto vis = [&](int i) {
+          const int c0 = k0 + 32 * i;
+          uint32_t v = low_bits(hi - c0) & (~low_bits(lo - c0) | low_bits(first - c0));
+          if (bad != 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c0 = k0 + 32 * i;
-            vis[i] = low_bits(hi - c0) & (~low_bits(lo - c0) | low_bits(first - c0));
-            if (bad != 0) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (bad >> (n_pg > 1 ? (32 * i + 16 * h) >> page_shift : 0) & 1) vis[i] &= h ? 0x0000ffffu : 0xffff0000u;
-            }
+            for (int h = 0; h < 2; ++h)
+              if (bad >> (n_pg > 1 ? (32 * i + 16 * h) >> page_shift : 0) & 1) v &= h ? 0x0000ffffu : 0xffff0000u;
           }
-        }
-        ok = wait_bar(bar(kBS + wg), (tau >> 1) & 1, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+          return v;
+        };
+        const uint32_t s_addr = lanes + kColS + 128 * (tau & 1) + 64 * half;
+        wait(kBS + (tau & 1), (tau >> 1) & 1);
         fence_after();
-        float top = -INFINITY;
         if (live) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float s[32];
-            tmem_ld32(s_addr + 32 * i, s);
+          // P against the maximum before this tile; once more only if that has to move
+          float top = -INFINITY, sum;
+          uint32_t pk[32];
+          const float m_old = m;
+          for (bool again = false;; again = true) {
+            const float base = m == -INFINITY ? 0.f : m;
+            float s[64], l0 = 0.f, l1 = 0.f;
+            tmem_ld64(s_addr, s);
             if (edge) {
+              const uint32_t v0 = vis(2 * half), v1 = vis(2 * half + 1);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) top = fmaxf(top, vis[i] >> c & 1 ? s[c] : -INFINITY);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
-            }
-          }
-          top *= scale_log2;
-        }
-        // the running maximum after the tile before, from the other group
-        float m_prev = -INFINITY;
-        if (y > 0) {
-          ok = wait_bar(bar(kBM + 4 * (wg ^ 1) + wq), ((tau - 1) >> 1) & 1, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          m_prev = sM[(wg ^ 1) * kRows + row];
-        }
-        const float m_new = top > m_prev + kLag ? top : m_prev;
-        sM[wg * kRows + row] = m_new;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBM + 4 * wg + wq));
-        if (live) {
-          // O holds sums against m_prev: rescale the rows whose maximum jumped
-          const bool jump = y > 0 && m_new != m_prev && m_prev != -INFINITY;
-          if (__any_sync(0xffffffffu, jump)) {
-            ok = wait_bar(bar(kBPv + ((tau - 1) & 1)), ((tau - 1) >> 1) & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            fence_after();
-            const float f = jump ? exp2_fast(m_prev - m_new) : 1.f;
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-              float o[32];
-              tmem_ld32(tmem + lanes + 32 * i, o);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] *= f;
-              tmem_st32(tmem + lanes + 32 * i, o);
-            }
-          }
-          if (m_new != m) l *= exp2_fast(m - m_new);
-          m = m_new;
-          const float base = m_new == -INFINITY ? 0.f : m_new;
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float s[32];
-            uint32_t pk[16];
-            tmem_ld32(s_addr + 32 * i, s);
-            if (edge) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) s[c] = vis[i] >> c & 1 ? s[c] : -INFINITY;
+              for (int c = 0; c < 32; ++c) {
+                s[c] = v0 >> c & 1 ? s[c] : -INFINITY;
+                s[32 + c] = v1 >> c & 1 ? s[32 + c] : -INFINITY;
+              }
             }
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
+            for (int c = 0; c < 64; c += 2) {
+              top = fmaxf(top, fmaxf(s[c], s[c + 1]));
               const float p0 = exp2_fast(fmaf(s[c], scale_log2, -base));
               const float p1 = exp2_fast(fmaf(s[c + 1], scale_log2, -base));
               l0 += p0;
               l1 += p1;
               pk[c >> 1] = pack_bf16(p0, p1);
             }
-            tmem_st16(s_addr + 16 * i, pk);
+            sum = l0 + l1;
+            if (again) break;
+            top = fmaxf(top * scale_log2, other(top * scale_log2));
+            if (top > m + kLag) m = top;
+            if (!__any_sync(0xffffffffu, m != m_old)) break;
           }
-          l += l0 + l1;
+          // O holds sums against m_old: this half of the dims, where the maximum moved
+          const bool jump = y > 0 && m != m_old && m_old != -INFINITY;
+          if (__any_sync(0xffffffffu, jump)) {
+            wait(kBPv + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
+            fence_after();
+            const float f = jump ? exp2_fast(m_old - m) : 1.f;
+#pragma unroll 1
+            for (int i = 4 * half; i < 4 * half + 4; ++i) {
+              float o[32];
+              tmem_ld32(lanes + 32 * i, o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= f;
+              tmem_st32(lanes + 32 * i, o);
+            }
+          }
+          if (m != m_old) l *= exp2_fast(m_old - m);
+          l += sum;
+          tmem_st32(s_addr, pk);
           tmem_st_wait();
         }
         if (edge) {
-          // this thread's key of the tile: V rows that not every query row sees
+          // this thread's key of the tile and half of its dims: V rows that not every query row sees
           const int j = k0 + row;
           const bool page_ok = !(bad >> (n_pg > 1 ? row >> page_shift : 0) & 1);
           const bool any = page_ok && j < w.it.hi1 && (j >= w.it.lo0 || j < first);
           const bool all = page_ok && j < w.it.hi0 && (j >= w.it.lo1 || j < first);
-          // V of tile y follows K of tile y + 1: units 4 (2 y + 2) on, the last tile's four earlier
-          const uint32_t u = units + (y + 1 < n ? 8 * y + 8 : 8 * y + 4) + (row >> 5);
-          ok = wait_bar(bar(kBFull + u % kUnits), (u / kUnits) & 1, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          uint8_t* vr = smem + kOffRing + (u % kUnits) * kUnitBytes + (row & 31) * 128;
+          // V of tile y follows K of tile y + 1: its two units are 4 y + 4 on, the last tile's 4 y + 2
+          const uint32_t u = units + (y + 1 < n ? 4 * y + 4 : 4 * y + 2) + (row >> 6);
+          wait(kBFull + u % kUnits, (u / kUnits) & 1);
+          uint8_t* vr = smem + kOffRing + (u % kUnits) * kUnitBytes + ((row >> 5) & 1) * kSubBytes + (row & 31) * 128;
           if (!all) {
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 16 * half; i < 16 * half + 16; ++i) {
               uint4* x = reinterpret_cast<uint4*>(vr + (i >> 3) * 4096 + (((i & 7) ^ (lane & 7)) << 4));
               if (!any) {
                 *x = make_uint4(0, 0, 0, 0);
@@ -747,7 +805,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               }
               if (changed) {
                 *x = val;
-                poison[w.k & 1] = 1;
+                poison[w.k % 3] = 1;
               }
             }
           }
@@ -755,28 +813,15 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBP + wg));
+        if (lane == 0) mbar_arrive(bar(kBP + (tau & 1)));
       }
-      units += 8 * n;
-      if (!ok) break;
-      // ---- epilogue: the two groups' row sums, then half of the dims each
-      const int last = (tau - 1) & 1;
-      if (!both()) break;  // both groups are past the previous epilogue's reads
-      if (wg != last) sL[row] = l;
-      if (tid == 0) poison[(w.k + 1) & 1] = 0;
-      if (!both()) break;
-      const float m_fin = sM[last * kRows + row];
-      if (wg == last) {
-        const float lo_ = sL[row];
-        if (lo_ != 0.f) l += lo_ * exp2_fast(sM[(wg ^ 1) * kRows + row] - m_fin);
-        sL[row] = l;
-      }
-      const bool poisoned = poison[w.k & 1] != 0;
-      if (!both()) break;
-      const float total = sL[row];
-      ok = wait_bar(bar(kBPv + last), ((tau - 1) >> 1) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      units += 4 * n;
+      // ---- epilogue: the row's sum, then half of the dims each
+      if (tid == 0) poison[(w.k + 1) % 3] = 0;  // last read two items ago
+      bar_sync(5, 256);                          // every thread's part of poison[k % 3] is in
+      const bool poisoned = poison[w.k % 3] != 0;
+      const float total = half == 0 ? l + other(l) : other(l) + l;  // the same sum in both
+      wait(kBPv + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
       fence_after();
       if (live) {
         const bool whole = w.x0 == 0 && w.x1 == w.it.n;
@@ -785,9 +830,9 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         const int slot = 2 * static_cast<int>(blockIdx.x) + (w.x0 == 0 ? 1 : 0);
         const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll 1
-        for (int i = 4 * wg; i < 4 * wg + 4; ++i) {
+        for (int i = 4 * half; i < 4 * half + 4; ++i) {
           float o[32];
-          tmem_ld32(tmem + lanes + 32 * i, o);
+          tmem_ld32(lanes + 32 * i, o);
           if (poisoned && row < w.it.rows) {
             // non-finite V elements taken out of the product, back where they are seen
             const __nv_bfloat16* vp = v_pool + w.g * kHeadDim + 32 * i;
@@ -824,9 +869,9 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           }
           __syncwarp();
         }
-        if (wg == last && row < w.it.rows) {
-          if (whole) lse[orow] = total == 0.f ? -INFINITY : (m_fin + log2f(total)) * kLn2;
-          else part_ml[slot * kRows + row] = make_float2(m_fin, total);
+        if (half == 0 && row < w.it.rows) {
+          if (whole) lse[orow] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
+          else part_ml[slot * kRows + row] = make_float2(m, total);
         }
       }
       if (tid == 0 && w.x0 == 0 && w.x1 < w.it.n) {  // the item goes on in the ranges behind this one
@@ -847,15 +892,15 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512));
+  if (warp == kMmaS) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512));
   if (tid == 0 && *abort_flag) cont[blockIdx.x].status = 2;
 }
 
-// Joins the parts of the item that CTA range blockIdx.x begins and does not
-// end: block row y takes the item's rows y, y + gridDim.y, ..., its eight
-// warps an eighth of the parts each, added in order.  Also gathers the ranges'
-// status into the call's.
-constexpr int kJoinWarps = 8, kJoinRows = 16;
+// Joins the parts of the item that CTA range blockIdx.x begins and does not end.  An item of
+// many rows has few parts: a warp takes a row (row 8 y + warp of block y).  One with many parts (few
+// rows, a long cache): a block takes row y, y + 16, ..., its warps an eighth of the parts each,
+// added in order.  Also gathers the ranges' status into the call's.
+constexpr int kJoinWarps = 8, kJoinBlocks = kRows / kJoinWarps;
 __global__ void __launch_bounds__(kJoinWarps * 32)
 causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ part_ml, const Cont* __restrict__ cont,
                    int G, int* __restrict__ status, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
@@ -870,16 +915,17 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
     if (threadIdx.x == 0) *status = bad ? 2 : 0;
   }
   const Cont ct = cont[c0];
+  if (ct.rows == 0) return;
   const int n = ct.c_last - c0 + 1;  // part 0: slot (c0, 1), part i: slot (c0 + i, 0)
   auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
-  for (int r = blockIdx.y; r < ct.rows; r += gridDim.y) {
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, part_ml[slot(i) * kRows + r].x);
+  // this warp's sums (dims 8 lane on) of parts [a, z) of row r against the row's maximum m
+  float o[8], l;
+  auto add = [&](int r, int a, int z, float m) {
+    l = 0.f;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    float l = 0.f, o[8] = {};
+    for (int i = 0; i < 8; ++i) o[i] = 0.f;
 #pragma unroll 4
-    for (int i = n * warp / kJoinWarps; i < n * (warp + 1) / kJoinWarps; ++i) {
+    for (int i = a; i < z; ++i) {
       const float2 ml = part_ml[slot(i) * kRows + r];
       const float4* p = reinterpret_cast<const float4*>(part + static_cast<int64_t>(slot(i)) * kPartFloats + r * kHeadDim) +
                         2 * lane;
@@ -889,6 +935,35 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
       o[0] += u.x * f, o[1] += u.y * f, o[2] += u.z * f, o[3] += u.w * f;
       o[4] += v.x * f, o[5] += v.y * f, o[6] += v.z * f, o[7] += v.w * f;
     }
+  };
+  auto max_of = [&](int r) {
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part_ml[slot(i) * kRows + r].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    return m;
+  };
+  auto row_of = [&](int r) {
+    const int f = ct.first + r;
+    return (static_cast<int64_t>(ct.row0) + f / kHeadsPerGroup) * G * kHeadsPerGroup + ct.g * kHeadsPerGroup +
+           f % kHeadsPerGroup;
+  };
+  if (n <= kJoinWarps) {
+    const int r = kJoinWarps * blockIdx.y + warp;
+    if (r >= ct.rows) return;
+    const float m = max_of(r);
+    add(r, 0, n, m);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t row = row_of(r);
+    *reinterpret_cast<uint4*>(out + row * kHeadDim + 8 * lane) =
+        make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                   pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+    if (lane == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    return;
+  }
+  for (int r = blockIdx.y; r < ct.rows; r += kJoinBlocks) {
+    const float m = max_of(r);
+    add(r, n * warp / kJoinWarps, n * (warp + 1) / kJoinWarps, m);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) sO[warp][8 * lane + i] = o[i];
@@ -900,11 +975,9 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
       total += sL[x];
       y += sO[x][threadIdx.x];
     }
-    const int f = ct.first + r;
-    const int64_t orow = (static_cast<int64_t>(ct.row0) + f / kHeadsPerGroup) * G * kHeadsPerGroup +
-                         ct.g * kHeadsPerGroup + f % kHeadsPerGroup;
-    out[orow * kHeadDim + threadIdx.x] = __float2bfloat16_rn(total == 0.f ? 0.f : y / total);
-    if (threadIdx.x == 0) lse[orow] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
+    const int64_t row = row_of(r);
+    out[row * kHeadDim + threadIdx.x] = __float2bfloat16_rn(total == 0.f ? 0.f : y / total);
+    if (threadIdx.x == 0) lse[row] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
   }
 }
 
@@ -952,7 +1025,7 @@ cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* 
                                               scale * kLog2e, part, ml, cont, static_cast<__nv_bfloat16*>(out), lse);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  causal_join_kernel<<<dim3(grid, kJoinRows), kJoinWarps * 32, 0, s>>>(part, ml, cont, G, status,
+  causal_join_kernel<<<dim3(grid, kJoinBlocks), kJoinWarps * 32, 0, s>>>(part, ml, cont, G, status,
                                                                       static_cast<__nv_bfloat16*>(out), lse);
   return cudaGetLastError();
 }
