@@ -196,12 +196,10 @@ qsa_status_t qsa_paged_forward(const void* q, const void* k_pages, const void* v
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int32_t* row_cnt = at<int32_t>(workspace, L.row_cnt);
   int32_t* row_cols = at<int32_t>(workspace, L.row_cols);
-  QSA_TRY(qsa::launch_route_rows(routes, T, max_pages * page_size, n_sel, row_cnt, row_cols, nullptr, 2,
-                                 at<int>(workspace, L.status), nullptr, nullptr, nullptr, H, nullptr, s));
-  QSA_TRY(qsa::launch_paged_forward(q, k_pages, v_pages,
-                                    view(block_table, kv_len, cu_q, B, n_pages, page_size, max_pages), row_cnt,
-                                    row_cols, T, G, n_sel, scale, L.splits, at<void>(workspace, L.partial), out, lse,
-                                    s));
+  QSA_TRY(qsa::launch_paged_rows(routes, view(block_table, kv_len, cu_q, B, n_pages, page_size, max_pages), T, n_sel,
+                                 at<int>(workspace, L.status), row_cnt, row_cols, s));
+  QSA_TRY(qsa::launch_paged_forward(q, k_pages, v_pages, row_cnt, row_cols, T, G, n_sel, scale, L.splits,
+                                    at<void>(workspace, L.partial), out, lse, s));
   return QSA_OK;
 }
 

@@ -50,7 +50,7 @@ constexpr int kTileKeys = 128;
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kMmaS = 9, kMmaO = 10, kLoader = 11;  // warps
 constexpr int kUnits = 5;                      // ring units
-constexpr int kSubBytes = 16384;               // K: [128 keys][64 dims]; V: [32 keys][256 dims]
+constexpr int kSubBytes = 16384;               // K: [128 keys][64 dims]; V: 32 keys of 256 dims
 constexpr int kUnitBytes = 2 * kSubBytes;
 constexpr int kOffRing = kRows * 512;          // Q: four [128][64] blocks, 128-byte swizzle
 constexpr int kOffX = kOffRing + kUnits * kUnitBytes;  // [2][2][128] floats that a row's threads exchange
@@ -100,7 +100,7 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   return s;
 }
 __device__ __forceinline__ int query_tiles(const Seq& s) {
-  return static_cast<int>((static_cast<int64_t>(s.n) * kHeadsPerGroup + kRows - 1) / kRows);
+  return (s.n * kHeadsPerGroup - 1) / kRows + (s.n > 0 ? 1 : 0);
 }
 __device__ __forceinline__ int64_t key_limit(const Args& a) {
   return static_cast<int64_t>(a.c.max_pages) << a.c.page_shift;
@@ -124,8 +124,8 @@ struct Item {         // what query tile i of a sequence sees
 };
 __device__ __forceinline__ Item item_of(const Args& a, const Seq& s, int i) {
   Item it;
-  const int64_t r0 = static_cast<int64_t>(i) * kRows, r_end = static_cast<int64_t>(s.n) * kHeadsPerGroup;
-  it.rows = static_cast<int>(min(static_cast<int64_t>(kRows), r_end - r0));
+  const int r0 = i * kRows;  // below n * 12 <= T * H, which fits 31 bits
+  it.rows = min(kRows, s.n * kHeadsPerGroup - r0);
   const int64_t pa = s.p0 + r0 / kHeadsPerGroup, pz = s.p0 + (r0 + it.rows - 1) / kHeadsPerGroup;
   it.hi0 = row_hi(a, pa);
   it.hi1 = row_hi(a, pz);
@@ -139,6 +139,8 @@ __device__ __forceinline__ Item item_of(const Args& a, const Seq& s, int i) {
   it.n = max(it.n_first + n_w, 1);
   return it;
 }
+// V lies in runs of neighbouring keys, [four 64-dim blocks][run][64 dims]: 32 keys, or a 16-key page.
+__device__ __forceinline__ int v_run(const Args& a) { return a.c.page_shift == 4 ? 16 : 32; }
 __device__ __forceinline__ int key_tile(const Item& it, int x) {
   return x < it.n_first ? x : it.w_first + x - it.n_first;
 }
@@ -240,8 +242,9 @@ __device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {  // 128-byte s
   return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(1) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
-__device__ __forceinline__ uint64_t desc_v(uint32_t addr) {  // MN-major: 64-dim blocks 4096 bytes apart, 8-key groups 1024
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(4096 >> 4) << 16) |
+// MN-major: 64-dim blocks `run` keys (of 128 bytes) apart, 8-key groups 1024 bytes
+__device__ __forceinline__ uint64_t desc_v(uint32_t addr, int run) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(run * 128 >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
@@ -403,6 +406,10 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
   int* start = reinterpret_cast<int*>(smem + kOffStart);
   auto bar = [&](int i) { return sb + kOffBar + 8 * i; };
 
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(&k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(&v_map) : "memory");
+  }
   // ---- the CTA's range of tiles (scratch in the ring, before any copy)
   int64_t t_begin = 0, t_end = 0, n_tiles = 0;
   int n_ctas = 1;
@@ -410,13 +417,15 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     int* pre = reinterpret_cast<int*>(smem + kOffRing);
     long long* sums = reinterpret_cast<long long*>(smem + kOffRing + 4096);
     long long mine = 0, all = 0;
-    each_batch(a, pre, sums, [&](int, int, long long w) {
+    int batches = 0, seq0 = -1, tile0 = 0;  // the last batch's query tile of this thread
+    long long w0 = 0;
+    each_batch(a, pre, sums, [&](int seq, int i, long long w) {
       mine += w;
+      ++batches;
+      seq0 = seq, tile0 = i, w0 = w;
       return false;
     });
-    __syncthreads();
-    block_scan<long long>(mine, sums, all);
-    __syncthreads();
+    const long long incl0 = block_scan<long long>(mine, sums, all);
     n_tiles = all;
     n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(n_tiles / kMinTiles, static_cast<int64_t>(1))));
     const int c = static_cast<int>(blockIdx.x);
@@ -429,21 +438,26 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     if (n_tiles == 0 || c >= n_ctas || !aligned) return;  // uniform
     t_begin = n_tiles * c / n_ctas;
     t_end = n_tiles * (c + 1) / n_ctas;
-    long long base = 0;
-    each_batch(a, pre, sums, [&](int seq, int i, long long w) {
-      long long batch;
-      const long long incl = block_scan<long long>(w, sums, batch);
-      const long long at = base + incl - w;
-      if (t_begin >= at && t_begin < at + w) {
-        const int n = static_cast<int>(w / a.G), off = static_cast<int>(t_begin - at);
-        start[0] = seq;
-        start[1] = i;
-        start[2] = off / n;
-        start[3] = off % n;
-      }
-      base += batch;
-      return base > t_begin;
-    });
+    auto locate = [&](int seq, int i, long long w, long long at) {  // if the range begins in this query tile
+      if (t_begin < at || t_begin >= at + w) return;
+      const int n = static_cast<int>(w / a.G), off = static_cast<int>(t_begin - at);
+      start[0] = seq;
+      start[1] = i;
+      start[2] = off / n;
+      start[3] = off % n;
+    };
+    if (batches == 1) {  // what the scan above has in hand
+      locate(seq0, tile0, w0, incl0 - w0);
+    } else {
+      long long base = 0;
+      each_batch(a, pre, sums, [&](int seq, int i, long long w) {
+        long long batch;
+        const long long incl = block_scan<long long>(w, sums, batch);
+        locate(seq, i, w, base + incl - w);
+        base += batch;
+        return base > t_begin;
+      });
+    }
   }
   if (tid == 0) {
     for (int i = 0; i < kUnits; ++i) {
@@ -480,7 +494,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     const int page_shift = a.c.page_shift, page = 1 << page_shift;
     const int n_pg = page < kTileKeys ? kTileKeys >> page_shift : 1;  // pages per tile
     const int no_row = a.c.n_pages << page_shift;                      // past the pool: TMA fills zeros
-    const int k_box = min(page, kTileKeys);
+    const int k_box = min(page, kTileKeys), run = v_run(a);
     Ring ring;
     uint32_t issued = 0;
     bool ok = true;
@@ -519,18 +533,12 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         claim();
         if (!ok) return;
         const uint32_t dst = sb + kOffRing + ring.slot * kUnitBytes;
-        if (page >= 32) {  // lane = run of 32 keys
-          const int key = 64 * u + 32 * (lane & 1), from = page < kTileKeys ? key >> page_shift : 0;
-          const int r = __shfl_sync(0xffffffffu, rows, from);
-          if (lane < 2)
-            tma_load(dst + lane * kSubBytes, &v_map, r == no_row ? no_row : r + key - (from << page_shift), 0, w.g,
-                     bar(kBFull + ring.slot));
-        } else {  // 16-key pages: lane = page * 4 + block of 64 dims
-          const int r = __shfl_sync(0xffffffffu, rows, 4 * u + ((lane >> 2) & 3));
-          if (lane < 16)
-            tma_load(dst + (lane >> 3) * kSubBytes + ((lane >> 2) & 1) * 2048 + (lane & 3) * 4096, &v_map, r, lane & 3,
-                     w.g, bar(kBFull + ring.slot));
-        }
+        // lane = run of keys
+        const int key = 64 * u + run * (lane & 3), from = page < kTileKeys ? (key & 127) >> page_shift : 0;
+        const int r = __shfl_sync(0xffffffffu, rows, from);
+        if (lane < 64 / run)
+          tma_load(dst + lane * run * 512, &v_map, r == no_row ? no_row : r + key - (from << page_shift), 0, w.g,
+                   bar(kBFull + ring.slot));
         ring.step();
       }
     };
@@ -598,7 +606,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           ring.step(2);               // V of the last tile
         } while (ok && w.next(a));
       } else {
-        const uint64_t v_desc = desc_v(sb + kOffRing);
+        const int run = v_run(a);
+        const uint64_t v_desc = desc_v(sb + kOffRing, run);
         do {
           const int n = w.x1 - w.x0;
           ring.step(n > 1 ? 4 : 2);   // K of the first two tiles
@@ -614,8 +623,9 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               fence_after();
               const uint64_t vd = v_desc + ring.slot * (kUnitBytes >> 4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_ts(tmem, p + 64 * u + 8 * i, vd + (i >> 1) * (kSubBytes >> 4) + (i & 1) * (2048 >> 4),
+              for (int i = 0; i < 4; ++i)  // 16 keys: a run, or half of one
+                mma_ts(tmem, p + 64 * u + 8 * i,
+                       vd + (run == 16 ? i * (8192 >> 4) : (i >> 1) * (kSubBytes >> 4) + (i & 1) * (2048 >> 4)),
                        y > 0 || u > 0 || i > 0);
               commit(bar(kBEmpty + ring.slot));
               ring.step();
@@ -641,15 +651,22 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     do {
       if (w.k > 0) ok = warp_wait(bar(kBQEmpty), (w.k - 1) & 1, abort_flag);
       if (!ok) break;
-      // a warp copies whole 512-byte rows; rows past the last are zeros up to the 32 of a softmax warp
-      const int n = min(kRows, (w.it.rows + 31) & ~31);
-      const int64_t r0 = static_cast<int64_t>(w.i) * kRows;
+      // a 512-byte row an instruction; rows past the last are zeros up to the 32 of a softmax warp
+      const int n = min(kRows, (w.it.rows + 31) & ~31), r0 = w.i * kRows;
+      int h = r0 % kHeadsPerGroup;
+      const __nv_bfloat16* src = q + ((static_cast<int64_t>(w.s.start) + r0 / kHeadsPerGroup) * H +
+                                      w.g * kHeadsPerGroup + h) * kHeadDim + lane * 8;
+      const int64_t to_next_token = static_cast<int64_t>(H - kHeadsPerGroup + 1) * kHeadDim;
+      const uint32_t dst = sb + (lane >> 3) * (kRows * 128);
+#pragma unroll 4
       for (int r = 0; r < n; ++r) {
-        const int64_t f = r0 + min(r, w.it.rows - 1);
-        const int64_t t = w.s.start + f / kHeadsPerGroup;
-        const __nv_bfloat16* src =
-            q + (t * H + w.g * kHeadsPerGroup + f % kHeadsPerGroup) * kHeadDim + lane * 8;
-        cp_async16(sb + (lane >> 3) * (kRows * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src, r < w.it.rows);
+        cp_async16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src, r < w.it.rows);
+        if (++h == kHeadsPerGroup) {
+          h = 0;
+          src += to_next_token;
+        } else {
+          src += kHeadDim;
+        }
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -785,10 +802,11 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           // V of tile y follows K of tile y + 1: its two units are 4 y + 4 on, the last tile's 4 y + 2
           const uint32_t u = units + (y + 1 < n ? 4 * y + 4 : 4 * y + 2) + (row >> 6);
           wait(kBFull + u % kUnits, (u / kUnits) & 1);
-          uint8_t* vr = smem + kOffRing + (u % kUnits) * kUnitBytes + ((row >> 5) & 1) * kSubBytes + (row & 31) * 128;
+          const int run = v_run(a), in_unit = row & 63;
+          uint8_t* vr = smem + kOffRing + (u % kUnits) * kUnitBytes + in_unit / run * run * 512 + in_unit % run * 128;
           if (!all) {
             for (int i = 16 * half; i < 16 * half + 16; ++i) {
-              uint4* x = reinterpret_cast<uint4*>(vr + (i >> 3) * 4096 + (((i & 7) ^ (lane & 7)) << 4));
+              uint4* x = reinterpret_cast<uint4*>(vr + (i >> 3) * run * 128 + (((i & 7) ^ (lane & 7)) << 4));
               if (!any) {
                 *x = make_uint4(0, 0, 0, 0);
                 continue;
@@ -897,10 +915,11 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
 }
 
 // Joins the parts of the item that CTA range blockIdx.x begins and does not end.  An item of
-// many rows has few parts: a warp takes a row (row 8 y + warp of block y).  One with many parts (few
-// rows, a long cache): a block takes row y, y + 16, ..., its warps an eighth of the parts each,
+// many rows has few parts: a warp takes a row (row 16 y + warp of block y).  One with many parts (few
+// rows, a long cache): a block takes row y, y + 12, ..., its warps a sixteenth of the parts each,
 // added in order.  Also gathers the ranges' status into the call's.
-constexpr int kJoinWarps = 8, kJoinBlocks = kRows / kJoinWarps;
+constexpr int kJoinWarps = 16, kJoinBlocks = kHeadsPerGroup;
+static_assert(kJoinWarps * kJoinBlocks >= kRows, "a warp per row");
 __global__ void __launch_bounds__(kJoinWarps * 32)
 causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ part_ml, const Cont* __restrict__ cont,
                    int G, int* __restrict__ status, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
@@ -924,7 +943,7 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
     l = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = a; i < z; ++i) {
       const float2 ml = part_ml[slot(i) * kRows + r];
       const float4* p = reinterpret_cast<const float4*>(part + static_cast<int64_t>(slot(i)) * kPartFloats + r * kHeadDim) +
@@ -969,6 +988,7 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
     for (int i = 0; i < 8; ++i) sO[warp][8 * lane + i] = o[i];
     if (lane == 0) sL[warp] = l;
     __syncthreads();
+    if (threadIdx.x >= kHeadDim) continue;
     float total = 0.f, y = 0.f;
 #pragma unroll
     for (int x = 0; x < kJoinWarps; ++x) {
@@ -1011,7 +1031,7 @@ cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* 
   const uint32_t page = 1u << c.page_shift;
   const uint64_t rows = static_cast<uint64_t>(c.n_pages) << c.page_shift;
   if (!encode_pool(&k_map, k_pages, rows, G, page < kTileKeys ? page : kTileKeys, 1) ||
-      !encode_pool(&v_map, v_pages, rows, G, page < 32 ? page : 32, page < 32 ? 1 : 4))
+      !encode_pool(&v_map, v_pages, rows, G, page < 32 ? page : 32, 4))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(causal_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;

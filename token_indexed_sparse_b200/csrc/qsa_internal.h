@@ -132,15 +132,17 @@ cudaError_t launch_cache_append(const HeadRows& q, const HeadRows& k, const Head
                                 void* k_pages, void* v_pages, const CacheView& c, const double* inv_freq, int64_t T,
                                 int nq, int G, int rot, bool inter, float m, cudaStream_t s);
 
-// Attention of a packed batch's new tokens over the pages by sorted route lists (qsa_paged.cu):
-// row_cnt / row_cols as launch_route_rows writes them for IDs below max_pages * page_size.
-// `splits` parts of every row's keys go to `partial` (paged_partial_bytes) and
-// are joined when it is above 1.
+// Route-set attention of a packed batch's new tokens over the pages (qsa_paged.cu): the pool rows
+// of every row's set (row_cnt [T], -1 for a row of no sequence; row_cols [T, n_sel]; *status zeroed),
+// then the attention over them in `splits` parts per row, joined from `partial`
+// (paged_partial_bytes) when it is above 1.
+cudaError_t launch_paged_rows(const int32_t* routes, const CacheView& c, int64_t T, int n_sel, int* status,
+                              int32_t* row_cnt, int32_t* row_cols, cudaStream_t s);
 int paged_splits(int64_t T, int G, int64_t max_keys);
 size_t paged_partial_bytes(int64_t T, int G, int splits);
-cudaError_t launch_paged_forward(const void* q, const void* k_pages, const void* v_pages, const CacheView& c,
-                                 const int32_t* row_cnt, const int32_t* row_cols, int64_t T, int G, int n_sel,
-                                 float scale, int splits, void* partial, void* out, float* lse, cudaStream_t s);
+cudaError_t launch_paged_forward(const void* q, const void* k_pages, const void* v_pages, const int32_t* row_cnt,
+                                 const int32_t* row_cols, int64_t T, int G, int n_sel, float scale, int splits,
+                                 void* partial, void* out, float* lse, cudaStream_t s);
 // Attention of a packed batch's new tokens over the keys j <= position with j > position - window
 // (when window > 0) or j < sinks (qsa_causal.cu).  `scratch`: causal_scratch_bytes, 256-byte aligned;
 // *status is set to 2 if a bounded wait gave up, else 0.

@@ -9,6 +9,7 @@ or the tensors are not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -89,7 +90,8 @@ def library() -> ctypes.CDLL:
     lib.qsa_cast_f32_to_bf16.restype = i32
     lib.qsa_cast_f32_to_bf16.argtypes = [vp, vp, i64, vp]
     rows = [vp, i64, i64]  # a [T, heads, 256] operand: pointer, token and head strides
-    cache = [vp, vp, vp, i64, i32, i64, i32, i64, i32, i32]  # table, kv_len, cu_q, T, B, n_pages, page_size, max_pages, H, G
+    # block_table, kv_len, cu_q, T, B, n_pages, page_size, max_pages, H, G
+    cache = [vp, vp, vp, i64, i32, i64, i32, i64, i32, i32]
     lib.qsa_rope.restype = i32
     lib.qsa_rope.argtypes = rows * 4 + [vp, vp, i64, i32, i32, i32, i32, f32, i32, vp]
     lib.qsa_cache_append.restype = i32
@@ -463,73 +465,83 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     return inv_freq.to(device), mscale
 
 
-def _on(device: torch.device, what: str, **tensors):
-    """All tensors (None: absent) on the CUDA device of the call."""
-    if device.type != "cuda":
-        raise ValueError(f"{what}: tensors must be CUDA tensors")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+# A decode step's calls take less time on the GPU than in here, so these helpers
+# read each property of a tensor once and raise from functions of their own.
+
+def _enqueue(index: int, what: str, named, call, *args):
+    """Runs a library call on CUDA device ``index`` (all tensors of ``named``,
+    pairs of name and tensor or None, have to be on it), its current stream last
+    in the arguments."""
+    for name, t in named:
+        if t is not None and t.get_device() != index or index < 0:
+            raise ValueError(f"{what}: {name} must be on {f'cuda:{index}' if index >= 0 else 'a CUDA device'}, "
+                             f"got {'nothing' if t is None else t.device}")
+    if index == torch._C._cuda_getDevice():
+        st = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != QSA_OK:
+        raise QSAError(st, what)
 
 
-def _enqueue(device: torch.device, what: str, call, *args):
-    """Runs a library call with ``device`` current, its stream last in the arguments."""
-    if device.index == torch.cuda.current_device():
-        _check(call(*args, _stream(device)), what)
-        return
-    with torch.cuda.device(device):
-        _check(call(*args, _stream(device)), what)
-
-
-def _rows(x: torch.Tensor, T: int | None, name: str):
-    """Pointer and strides of a ``[T, heads, 256]`` BF16 operand (dims contiguous, the rest as it is)."""
+def _bad_rows(x: torch.Tensor, T: int | None, name: str):
     if x.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
     if x.dim() != 3 or x.shape[2] != 256 or (T is not None and x.shape[0] != T):
         raise ValueError(f"{name} must be [{'T' if T is None else T}, heads, 256], got {tuple(x.shape)}")
-    if x.stride(2) != 1:
-        raise ValueError(f"{name} must have contiguous dims")
+    raise ValueError(f"{name} must have contiguous dims")
+
+
+def _rows(x: torch.Tensor, T: int | None, name: str):
+    """Pointer and strides of a ``[T, heads, 256]`` BF16 operand (dims contiguous, the rest as it is)."""
+    shape, stride = x.shape, x.stride()
+    if (x.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != 256 or stride[2] != 1
+            or (T is not None and shape[0] != T)):
+        _bad_rows(x, T, name)
     # the stride of an axis of length one is free
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0
+    return x.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
 def _rows_out(x: torch.Tensor, out: torch.Tensor | None, name: str) -> torch.Tensor:
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return torch.empty_like(x)
     if out.shape != x.shape:
         raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
     return out
 
 
-def _frequencies(inv_freq: torch.Tensor) -> int:
-    """Checks the rotary frequencies; returns rotary_dim."""
-    if inv_freq.dtype != torch.float64:
-        raise TypeError(f"inv_freq must be {torch.float64}, got {inv_freq.dtype}")
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous vector of rotary_dim / 2 frequencies")
-    return 2 * inv_freq.numel()
+def _vector(x: torch.Tensor, n: int | None, dtype, name: str):
+    """A contiguous vector (of ``n`` elements): its pointer."""
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.dim() != 1 or not x.is_contiguous() or (n is not None and x.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous vector{'' if n is None else f' of {n}'}, got {tuple(x.shape)}")
+    return x.data_ptr()
 
 
-def _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, backward, what):
-    lib = library()
-    T, H = q.shape[:2] if q.dim() == 3 else (0, 0)
+_NO_ROWS = (None, 0, 0)
+
+
+def _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, backward):
+    q_rows = _rows(q, None, "q")
+    T, H, _ = q.shape
     out_q = _rows_out(q, out_q, "out_q")
-    rows = [*_rows(q, None, "q"), 0, 0, 0, *_rows(out_q, T, "out_q"), 0, 0, 0]
+    k_rows = out_k_rows = _NO_ROWS
     G = 0
     if k is not None:
-        out_k = _rows_out(k, out_k, "out_k")
-        rows[3:6], rows[9:12] = _rows(k, T, "k"), _rows(out_k, T, "out_k")
+        k_rows = _rows(k, T, "k")
         G = k.shape[1]
+        out_k = _rows_out(k, out_k, "out_k")
+        out_k_rows = _rows(out_k, T, "out_k")
     elif out_k is not None:
         raise ValueError("out_k without k")
-    if positions.dtype != torch.int32:
-        raise TypeError(f"positions must be {torch.int32}, got {positions.dtype}")
-    if positions.shape != (T,) or not positions.is_contiguous():
-        raise ValueError(f"positions must be a contiguous [{T}] vector")
-    rot = _frequencies(inv_freq)
-    _on(q.device, what, k=k, out_q=out_q, out_k=out_k, positions=positions, inv_freq=inv_freq)
-    _enqueue(q.device, what, lib.qsa_rope, *rows, positions.data_ptr(), inv_freq.data_ptr(), T, H, G, rot,
-             1 if interleaved else 0, mscale, backward)
+    _enqueue(q.get_device(), "qsa_rope",
+             (("q", q), ("k", k), ("out_q", out_q), ("out_k", out_k), ("positions", positions),
+              ("inv_freq", inv_freq)),
+             library().qsa_rope, *q_rows, *k_rows, *_rows(out_q, T, "out_q"), *out_k_rows,
+             _vector(positions, T, torch.int32, "positions"), _vector(inv_freq, None, torch.float64, "inv_freq"), T, H,
+             G, 2 * inv_freq.shape[0], interleaved, mscale, backward)
     return out_q, out_k
 
 
@@ -540,17 +552,16 @@ def rope(q, k, positions, inv_freq, *, interleaved: bool = False, mscale: float 
     ``mscale`` as from ``rope_frequencies``; dims from rotary_dim up pass.  q and k
     may be slices of one projection (any strides between tokens and heads that
     are multiples of 8); ``out_q`` / ``out_k`` may be the inputs (in place)."""
-    return _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, 0, "qsa_rope")
+    return _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, 0)
 
 
 def rope_backward(grad_q, grad_k, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0,
                   out_q=None, out_k=None):
     """The gradient of ``rope``: ``(dq, dk)`` from the gradients of its outputs (the opposite turn)."""
-    return _rope(grad_q, grad_k, positions, inv_freq, interleaved, mscale, out_q, out_k, 1, "qsa_rope")
+    return _rope(grad_q, grad_k, positions, inv_freq, interleaved, mscale, out_q, out_k, 1)
 
 
-def _cache(k_pages, v_pages, block_table, kv_len, cu_q, T: int, H: int):
-    """Checks a cache; returns the arguments (table, kv_len, cu_q, T, B, n_pages, page_size, max_pages, H, G)."""
+def _bad_cache(k_pages, v_pages, block_table, kv_len, cu_q):
     for x, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
         if x.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
@@ -561,15 +572,20 @@ def _cache(k_pages, v_pages, block_table, kv_len, cu_q, T: int, H: int):
     for x, name in ((block_table, "block_table"), (kv_len, "kv_len"), (cu_q, "cu_q")):
         if x.dtype != torch.int32:
             raise TypeError(f"{name} must be {torch.int32}, got {x.dtype}")
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, max_pages = block_table.shape
-    if kv_len.shape != (B,) or cu_q.shape != (B + 1,):
-        raise ValueError(f"kv_len must be [{B}] and cu_q [{B + 1}]")
-    n_pages, page_size, G, _ = k_pages.shape
-    return (block_table.data_ptr(), kv_len.data_ptr(), cu_q.data_ptr(), T, B, n_pages, page_size, max_pages, H, G)
+    raise ValueError(f"block_table must be a contiguous [B, max_pages], got {tuple(block_table.shape)}")
+
+
+def _cache(k_pages, v_pages, block_table, kv_len, cu_q, T: int, H: int):
+    """Checks a cache; returns the arguments (table, kv_len, cu_q, T, B, n_pages, page_size, max_pages, H, G)."""
+    shape, table = k_pages.shape, block_table.shape
+    if (k_pages.dtype != torch.bfloat16 or v_pages.dtype != torch.bfloat16 or len(shape) != 4 or shape[3] != 256
+            or v_pages.shape != shape or not k_pages.is_contiguous() or not v_pages.is_contiguous()
+            or block_table.dtype != torch.int32 or len(table) != 2 or not block_table.is_contiguous()):
+        _bad_cache(k_pages, v_pages, block_table, kv_len, cu_q)
+    B = table[0]
+    return (block_table.data_ptr(), _vector(kv_len, B, torch.int32, "kv_len"),
+            _vector(cu_q, B + 1, torch.int32, "cu_q (one longer than kv_len)"),
+            T, B, shape[0], shape[1], table[1], H, shape[2])
 
 
 def cache_append(k_new, v_new, k_pages, v_pages, block_table, kv_len, cu_q, *, q=None, inv_freq=None,
@@ -579,46 +595,54 @@ def cache_append(k_new, v_new, k_pages, v_pages, block_table, kv_len, cu_q, *, q
     With ``inv_freq`` (see ``rope_frequencies``) k is turned to its position in
     the cache first, and ``q`` [T, H, 256] with it: returns the turned q (into
     ``out_q``, which may be q itself), else None."""
-    lib = library()
-    T, G = k_new.shape[:2] if k_new.dim() == 3 else (0, 0)
-    H = 12 * G
-    rows = [*_rows(k_new, None, "k_new"), *_rows(v_new, T, "v_new"), 0, 0, 0, 0, 0, 0]
-    if v_new.shape != k_new.shape:
+    k_rows = _rows(k_new, None, "k_new")
+    T, G, _ = k_new.shape
+    v_rows = _rows(v_new, T, "v_new")
+    if v_new.shape[1] != G:
         raise ValueError("k_new and v_new must have one shape")
+    H = 12 * G
+    q_rows = out_rows = _NO_ROWS
     if q is not None:
         if inv_freq is None:
             raise ValueError("q is only taken to be rotated: it needs inv_freq")
-        out_q = _rows_out(q, out_q, "out_q")
-        rows[6:9], rows[9:12] = _rows(q, T, "q"), _rows(out_q, T, "out_q")
+        q_rows = _rows(q, T, "q")
         H = q.shape[1]
+        out_q = _rows_out(q, out_q, "out_q")
+        out_rows = _rows(out_q, T, "out_q")
     elif out_q is not None:
         raise ValueError("out_q without q")
     cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
-    if k_pages.shape[2] != G:
-        raise ValueError(f"the pages hold {k_pages.shape[2]} KV heads, k_new {G}")
-    rot = _frequencies(inv_freq) if inv_freq is not None else 0
-    _on(k_new.device, "qsa_cache_append", v_new=v_new, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
-        kv_len=kv_len, cu_q=cu_q, q=q, inv_freq=inv_freq, out_q=out_q)
-    _enqueue(k_new.device, "qsa_cache_append", lib.qsa_cache_append, *rows,
-             inv_freq.data_ptr() if inv_freq is not None else None, rot, 1 if interleaved else 0, mscale,
+    if cache[9] != G:
+        raise ValueError(f"the pages hold {cache[9]} KV heads, k_new {G}")
+    freq, rot = None, 0
+    if inv_freq is not None:
+        freq, rot = _vector(inv_freq, None, torch.float64, "inv_freq"), 2 * inv_freq.shape[0]
+    _enqueue(k_new.get_device(), "qsa_cache_append",
+             (("k_new", k_new), ("v_new", v_new), ("k_pages", k_pages), ("v_pages", v_pages),
+              ("block_table", block_table), ("kv_len", kv_len), ("cu_q", cu_q), ("q", q), ("inv_freq", inv_freq),
+              ("out_q", out_q)),
+             library().qsa_cache_append, *k_rows, *v_rows, *q_rows, *out_rows, freq, rot, interleaved, mscale,
              k_pages.data_ptr(), v_pages.data_ptr(), *cache)
     return out_q
 
 
-def _paged_io(q, k_pages, out, lse):
+def _paged_io(q, out, lse):
     q = _prep(q, torch.bfloat16, "q")
-    if q.dim() != 3 or q.shape[2] != 256:
-        raise ValueError(f"q must be [T, H, 256], got {tuple(q.shape)}")
-    out = torch.empty_like(q) if out is None else _out(out, q.shape, torch.bfloat16, q.device, "out")
-    lse = (torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse is None
-           else _out(lse, q.shape[:2], torch.float32, q.device, "lse"))
-    return q, out, lse
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != 256:
+        raise ValueError(f"q must be [T, H, 256], got {tuple(shape)}")
+    out = torch.empty_like(q) if out is None else _out(out, shape, torch.bfloat16, q.device, "out")
+    lse = (torch.empty(shape[0], shape[1], dtype=torch.float32, device=q.device) if lse is None
+           else _out(lse, shape[:2], torch.float32, q.device, "lse"))
+    return q, out, lse, shape[0], shape[1]
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_forward_workspace_size(T, H, G, n_sel, page_size, max_pages) -> int:
     return int(library().qsa_paged_forward_workspace_size(T, H, G, n_sel, page_size, max_pages))
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_causal_workspace_size(T, H, G, page_size, max_pages, window: int = 0, sinks: int = 0) -> int:
     return int(library().qsa_paged_causal_workspace_size(T, H, G, page_size, max_pages, window, sinks))
 
@@ -631,21 +655,18 @@ def paged_forward(q, k_pages, v_pages, routes, block_table, kv_len, cu_q, scale:
     as in ``forward``).  Pools ``[n_pages, page_size, G, 256]``, ``block_table``
     [B, max_pages], ``kv_len`` [B] and ``cu_q`` [B + 1] int32.  Rows of no
     sequence are left as they were in ``out`` and ``lse``."""
-    lib = library()
-    q, out, lse = _paged_io(q, k_pages, out, lse)
+    q, out, lse, T, H = _paged_io(q, out, lse)
     routes = _prep(routes, torch.int32, "routes")
-    T, H = q.shape[:2]
     cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
     if routes.dim() != 2 or routes.shape[0] != T:
         raise ValueError("routes must have one row per query")
     n_sel = routes.shape[1]
-    _on(q.device, "qsa_paged_forward", k_pages=k_pages, v_pages=v_pages, routes=routes, block_table=block_table,
-        kv_len=kv_len, cu_q=cu_q)
-    ws = _workspace(lib.qsa_paged_forward_workspace_size(T, H, cache[9], n_sel, cache[6], cache[7]), q.device,
-                    workspace)
-    _enqueue(q.device, "qsa_paged_forward", lib.qsa_paged_forward, q.data_ptr(), k_pages.data_ptr(),
-             v_pages.data_ptr(), routes.data_ptr(), *cache, n_sel, scale, out.data_ptr(), lse.data_ptr(),
-             ws.data_ptr(), ws.numel())
+    ws = _workspace(paged_forward_workspace_size(T, H, cache[9], n_sel, cache[6], cache[7]), q.device, workspace)
+    _enqueue(q.get_device(), "qsa_paged_forward",
+             (("k_pages", k_pages), ("v_pages", v_pages), ("routes", routes), ("block_table", block_table),
+              ("kv_len", kv_len), ("cu_q", cu_q)),
+             library().qsa_paged_forward, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), routes.data_ptr(),
+             *cache, n_sel, scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse
 
 
@@ -656,15 +677,13 @@ def paged_causal(q, k_pages, v_pages, block_table, kv_len, cu_q, scale: float = 
     A token at position p sees the positions ``j <= p`` of its sequence, with
     ``window`` above 0 only those with ``j > p - window`` or ``j < sinks``.  The
     cache as in ``paged_forward``."""
-    lib = library()
-    q, out, lse = _paged_io(q, k_pages, out, lse)
-    T, H = q.shape[:2]
+    q, out, lse, T, H = _paged_io(q, out, lse)
     cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
-    _on(q.device, "qsa_paged_causal", k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
-        cu_q=cu_q)
-    ws = _workspace(lib.qsa_paged_causal_workspace_size(T, H, cache[9], cache[6], cache[7], window, sinks), q.device,
+    ws = _workspace(paged_causal_workspace_size(T, H, cache[9], cache[6], cache[7], window, sinks), q.device,
                     workspace)
-    _enqueue(q.device, "qsa_paged_causal", lib.qsa_paged_causal, q.data_ptr(), k_pages.data_ptr(),
-             v_pages.data_ptr(), *cache, window, sinks, scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-             ws.numel())
+    _enqueue(q.get_device(), "qsa_paged_causal",
+             (("k_pages", k_pages), ("v_pages", v_pages), ("block_table", block_table), ("kv_len", kv_len),
+              ("cu_q", cu_q)),
+             library().qsa_paged_causal, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *cache, window, sinks,
+             scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse
