@@ -57,7 +57,7 @@ constexpr int kOffX = kOffRing + kUnits * kUnitBytes;  // [2][2][128] floats tha
 constexpr int kOffBar = kOffX + 4 * kRows * 4;
 // barriers
 constexpr int kBFull = 0, kBEmpty = kBFull + kUnits, kBQFull = kBEmpty + kUnits, kBQEmpty = kBQFull + 1,
-              kBS = kBQEmpty + 1, kBP = kBS + 2, kBPv = kBP + 2, kBO = kBPv + 2, kBDrain = kBO + 1,
+              kBS = kBQEmpty + 1, kBP = kBS + 2, kBPv = kBP + 2, kBDrain = kBPv + 2,
               kBars = kBDrain + 2;
 constexpr int kOffTmem = kOffBar + kBars * 8;
 constexpr int kOffAbort = kOffTmem + 4;
@@ -471,7 +471,6 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       mbar_init(bar(kBP + i), 8);
       mbar_init(bar(kBPv + i), 1);
     }
-    mbar_init(bar(kBO), 8);
     mbar_init(bar(kBDrain), 1);
     mbar_init(bar(kBDrain + 1), 1);
     *abort_flag = 0;
@@ -584,12 +583,25 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
 #pragma unroll 1
           for (int y = 0; y < n && ok; ++y, ++tau) {
             const uint32_t s = tmem + kColS + 128 * (tau & 1);
-            if (tau >= 2) ok = wait(kBPv + (tau & 1), ((tau - 2) >> 1) & 1);  // P of tile tau - 2 has been read
+            // P of tile tau - 2 has been read (S of this tile goes over it); K's two units are there.
+            // A wait costs its thread 150 cycles even when it is over, so K's, which came long ago,
+            // come first.  They may not in an item's first two tiles: a parity tells a unit's use from
+            // the one before it only, so the slot's previous use (5 units earlier) must be known to have
+            // landed.  From the third tile on that is V of tile tau - 3, whose product the wait
+            // of the tile before saw end, and K of tile tau - 1; in the first two it is V of the item
+            // before, whose product the wait for tile tau - 2 sees end.
+            Ring second = ring;
+            second.step();
+            auto landed = [&]() {
+              return wait(kBFull + ring.slot, ring.phase) && wait(kBFull + second.slot, second.phase);
+            };
+            if (y >= 2) ok = landed();
+            if (ok && tau >= 2) ok = wait(kBPv + (tau & 1), ((tau - 2) >> 1) & 1);
+            if (ok && y < 2) ok = landed();
+            if (!ok) break;
+            fence_after();
 #pragma unroll 1
-            for (int u = 0; u < 2 && ok; ++u) {
-              ok = wait(kBFull + ring.slot, ring.phase);
-              if (!ok) break;
-              fence_after();
+            for (int u = 0; u < 2; ++u) {
               const uint64_t kd = k_desc + ring.slot * (kUnitBytes >> 4), qd = q_desc + u * (2 * kRows * 128 >> 4);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -598,7 +610,6 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               commit(bar(kBEmpty + ring.slot));
               ring.step();
             }
-            if (!ok) break;
             commit(bar(kBS + (tau & 1)));
             if (y > 0) ring.step(2);  // V of tile y - 1
           }
@@ -614,13 +625,17 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
 #pragma unroll 1
           for (int y = 0; y < n && ok; ++y, ++tau) {
             const uint32_t p = tmem + kColS + 128 * (tau & 1);
-            ok = wait(kBP + (tau & 1), (tau >> 1) & 1);
-            if (ok && y == 0 && w.k > 0) ok = wait(kBO, (w.k - 1) & 1);  // the sums before have been read
+            // What is over early first, P last.  S of this tile before V's units: their slots' previous
+            // uses are K of this tile and V of the tiles before it (see the parity note above).  An item's
+            // first P also says that the sums before have been read: the same threads do both.
+            Ring second = ring;
+            second.step();
+            ok = wait(kBS + (tau & 1), (tau >> 1) & 1) && wait(kBFull + ring.slot, ring.phase) &&
+                 wait(kBFull + second.slot, second.phase) && wait(kBP + (tau & 1), (tau >> 1) & 1);
+            if (!ok) break;
+            fence_after();
 #pragma unroll 1
-            for (int u = 0; u < 2 && ok; ++u) {
-              ok = wait(kBFull + ring.slot, ring.phase);
-              if (!ok) break;
-              fence_after();
+            for (int u = 0; u < 2; ++u) {
               const uint64_t vd = v_desc + ring.slot * (kUnitBytes >> 4);
 #pragma unroll
               for (int i = 0; i < 4; ++i)  // 16 keys: a run, or half of one
@@ -630,7 +645,6 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               commit(bar(kBEmpty + ring.slot));
               ring.step();
             }
-            if (!ok) break;
             commit(bar(kBPv + (tau & 1)));
             if (y + 2 < n) ring.step(2);  // K of tile y + 2
           }
@@ -694,11 +708,10 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     };
     // the other thread's value of the row (two buffers in turn: a buffer is written again only after
     // the exchange behind it, which both have reached)
-    auto other = [&](float x) {
-      volatile float* buf = sX + (ex++ & 1) * 2 * kRows;
-      buf[half * kRows + row] = x;
+    auto give = [&](float x) { sX[((ex & 1) * 2 + half) * kRows + row] = x; };
+    auto other = [&]() {
       bar_sync(1 + wq, 64);
-      return buf[(half ^ 1) * kRows + row];
+      return sX[((ex++ & 1) * 2 + (half ^ 1)) * kRows + row];
     };
     Walk w;
     w.begin(a, start, tiles);
@@ -758,9 +771,14 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 s[32 + c] = v1 >> c & 1 ? s[32 + c] : -INFINITY;
               }
             }
+            if (!again) {  // the other half's maximum comes while P is computed
+#pragma unroll
+              for (int c = 0; c < 64; c += 2) top = fmaxf(top, fmaxf(s[c], s[c + 1]));
+              top *= scale_log2;
+              give(top);
+            }
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
-              top = fmaxf(top, fmaxf(s[c], s[c + 1]));
               const float p0 = exp2_fast(fmaf(s[c], scale_log2, -base));
               const float p1 = exp2_fast(fmaf(s[c + 1], scale_log2, -base));
               l0 += p0;
@@ -769,7 +787,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             }
             sum = l0 + l1;
             if (again) break;
-            top = fmaxf(top * scale_log2, other(top * scale_log2));
+            top = fmaxf(top, other());
             if (top > m + kLag) m = top;
             if (!__any_sync(0xffffffffu, m != m_old)) break;
           }
@@ -801,6 +819,9 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           const bool all = page_ok && j < w.it.hi0 && (j >= w.it.lo1 || j < first);
           // V of tile y follows K of tile y + 1: its two units are 4 y + 4 on, the last tile's 4 y + 2
           const uint32_t u = units + (y + 1 < n ? 4 * y + 4 : 4 * y + 2) + (row >> 6);
+          // the slot may have held V of the tile before: only once that has been used does the unit's
+          // parity tell this use from that one
+          if (y > 0) wait(kBPv + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
           wait(kBFull + u % kUnits, (u / kUnits) & 1);
           const int run = v_run(a), in_unit = row & 63;
           uint8_t* vr = smem + kOffRing + (u % kUnits) * kUnitBytes + in_unit / run * run * 512 + in_unit % run * 128;
@@ -838,7 +859,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       if (tid == 0) poison[(w.k + 1) % 3] = 0;  // last read two items ago
       bar_sync(5, 256);                          // every thread's part of poison[k % 3] is in
       const bool poisoned = poison[w.k % 3] != 0;
-      const float total = half == 0 ? l + other(l) : other(l) + l;  // the same sum in both
+      give(l);
+      const float total = l + other();  // the same in both
       wait(kBPv + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
       fence_after();
       if (live) {
@@ -903,8 +925,6 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         cont[blockIdx.x] = ct;
       }
       fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBO));
     } while (w.next(a));
   }
   fence_before();
