@@ -65,7 +65,7 @@ constexpr int kOffPoison = kOffAbort + 4;      // [3]: the item saw non-finite V
 constexpr int kOffStart = kOffPoison + 12;     // the CTA's first tile: sequence, query tile, group, tile
 constexpr int kSmem = kOffStart + 16;          // no room to align the base: checked instead
 static_assert(kSmem <= 232448, "shared memory per block");
-constexpr uint32_t kSpin = 1u << 26;           // polls before a wait gives up (seconds)
+constexpr uint32_t kSpin = 1u << 22;           // polls before a wait gives up (seconds)
 constexpr uint32_t kColS = 256;                // tensor-memory columns: O [0, 256), S0, S1
 constexpr float kLag = 8.f;
 constexpr int kMinTiles = 2;                   // fewer tiles than this are not worth a CTA of their own
@@ -143,6 +143,12 @@ __device__ __forceinline__ Item item_of(const Args& a, const Seq& s, int i) {
 __device__ __forceinline__ int v_run(const Args& a) { return a.c.page_shift == 4 ? 16 : 32; }
 __device__ __forceinline__ int key_tile(const Item& it, int x) {
   return x < it.n_first ? x : it.w_first + x - it.n_first;
+}
+
+// Whether any row sees one of the 16 keys from `key` on (key 0's always count, so that every item has
+// a product that starts its sums): the steps that P V takes.
+__device__ __forceinline__ bool step_seen(const Item& it, int first, int key) {
+  return key == 0 || key < first || (key < it.hi1 && key + 16 > it.lo0);
 }
 
 // The CTA's walk: pieces (item, tiles [x0, x1)) of its range.  Every role walks alone.
@@ -336,21 +342,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
-// Bounded wait that also gives up once another role has.  It polls with test_wait: a thread that
-// try_wait has put to sleep for some thousands of cycles wakes up to a thousand late, which
-// every tile would pay several times over.
-__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
+// Bounded wait that also gives up once another role has.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  bool ok = test_bar(bar, parity);
+  bool ok = mbar_try(bar, parity);
 #pragma unroll 1
   for (uint32_t it = 0; !ok && it < kSpin; ++it) {
-    ok = test_bar(bar, parity);
+    ok = mbar_try(bar, parity);
     if ((it & 255) == 255 && *abort_flag) break;
   }
   if (!ok) *abort_flag = 1;
@@ -488,6 +485,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
   const int64_t tiles = t_end - t_begin;
 
+
   if (warp == kProducer) {
     // ------------------------------------------------------------ K / V units
     const int page_shift = a.c.page_shift, page = 1 << page_shift;
@@ -617,14 +615,19 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           ring.step(2);               // V of the last tile
         } while (ok && w.next(a));
       } else {
-        const int run = v_run(a);
+        const int run = v_run(a), first = first_keys(a);
         const uint64_t v_desc = desc_v(sb + kOffRing, run);
         do {
           const int n = w.x1 - w.x0;
+          bool summing = false;       // the item's first product starts its sums
           ring.step(n > 1 ? 4 : 2);   // K of the first two tiles
 #pragma unroll 1
           for (int y = 0; y < n && ok; ++y, ++tau) {
             const uint32_t p = tmem + kColS + 128 * (tau & 1);
+            const int k0 = key_tile(w.it, w.x0 + y) * kTileKeys;
+            uint32_t steps = 0;  // of 16 keys, those that some row sees
+#pragma unroll
+            for (int i = 0; i < 8; ++i) steps |= step_seen(w.it, first, k0 + 16 * i) ? 1u << i : 0u;
             // What is over early first, P last.  S of this tile before V's units: their slots' previous
             // uses are K of this tile and V of the tiles before it (see the parity note above).  An item's
             // first P also says that the sums before have been read: the same threads do both.
@@ -638,10 +641,12 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             for (int u = 0; u < 2; ++u) {
               const uint64_t vd = v_desc + ring.slot * (kUnitBytes >> 4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)  // 16 keys: a run, or half of one
+              for (int i = 0; i < 4; ++i) {  // 16 keys: a run, or half of one
+                if (!(steps >> (4 * u + i) & 1)) continue;
                 mma_ts(tmem, p + 64 * u + 8 * i,
-                       vd + (run == 16 ? i * (8192 >> 4) : (i >> 1) * (kSubBytes >> 4) + (i & 1) * (2048 >> 4)),
-                       y > 0 || u > 0 || i > 0);
+                       vd + (run == 16 ? i * (8192 >> 4) : (i >> 1) * (kSubBytes >> 4) + (i & 1) * (2048 >> 4)), summing);
+                summing = true;
+              }
               commit(bar(kBEmpty + ring.slot));
               ring.step();
             }
@@ -756,11 +761,10 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         fence_after();
         if (live) {
           // P against the maximum before this tile; once more only if that has to move
-          float top = -INFINITY, sum;
+          float sum, top = -INFINITY;
           uint32_t pk[32];
           const float m_old = m;
           for (bool again = false;; again = true) {
-            const float base = m == -INFINITY ? 0.f : m;
             float s[64], l0 = 0.f, l1 = 0.f;
             tmem_ld64(s_addr, s);
             if (edge) {
@@ -771,12 +775,14 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 s[32 + c] = v1 >> c & 1 ? s[32 + c] : -INFINITY;
               }
             }
-            if (!again) {  // the other half's maximum comes while P is computed
+            if (!again) {
 #pragma unroll
               for (int c = 0; c < 64; c += 2) top = fmaxf(top, fmaxf(s[c], s[c + 1]));
               top *= scale_log2;
-              give(top);
+              give(top);                            // the other half's maximum comes while P is computed,
+              if (y == 0) m = fmaxf(top, other());  // or is waited for: nothing is known yet
             }
+            const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               const float p0 = exp2_fast(fmaf(s[c], scale_log2, -base));
@@ -786,7 +792,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               pk[c >> 1] = pack_bf16(p0, p1);
             }
             sum = l0 + l1;
-            if (again) break;
+            if (again || y == 0) break;
             top = fmaxf(top, other());
             if (top > m + kLag) m = top;
             if (!__any_sync(0xffffffffu, m != m_old)) break;
@@ -812,7 +818,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           tmem_st_wait();
         }
         if (edge) {
-          // this thread's key of the tile and half of its dims: V rows that not every query row sees
+          // this thread's key of the tile and half of its dims: V rows that not every query row sees, in
+          // the steps that P V takes
           const int j = k0 + row;
           const bool page_ok = !(bad >> (n_pg > 1 ? row >> page_shift : 0) & 1);
           const bool any = page_ok && j < w.it.hi1 && (j >= w.it.lo0 || j < first);
@@ -825,7 +832,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           wait(kBFull + u % kUnits, (u / kUnits) & 1);
           const int run = v_run(a), in_unit = row & 63;
           uint8_t* vr = smem + kOffRing + (u % kUnits) * kUnitBytes + in_unit / run * run * 512 + in_unit % run * 128;
-          if (!all) {
+          if (!all && step_seen(w.it, first, j & ~15)) {
             for (int i = 16 * half; i < 16 * half + 16; ++i) {
               uint4* x = reinterpret_cast<uint4*>(vr + (i >> 3) * run * 128 + (((i & 7) ^ (lane & 7)) << 4));
               if (!any) {
@@ -865,10 +872,35 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       fence_after();
       if (live) {
         const bool whole = w.x0 == 0 && w.x1 == w.it.n;
-        const int64_t f = r0 + row;
-        const int64_t orow = (w.s.start + f / kHeadsPerGroup) * H + w.g * kHeadsPerGroup + f % kHeadsPerGroup;
+        // [T, H] row of a row of the tile
+        auto out_row = [&](int r) {
+          const int f = w.i * kRows + r, t = f / kHeadsPerGroup;
+          return (static_cast<int64_t>(w.s.start) + t) * H + w.g * kHeadsPerGroup + f - t * kHeadsPerGroup;
+        };
         const int slot = 2 * static_cast<int>(blockIdx.x) + (w.x0 == 0 ? 1 : 0);
         const float inv = total == 0.f ? 0.f : 1.f / total;
+        // Stores of whole rows by their threads would touch 32 lines each; so four lanes exchange the
+        // 16-byte pieces of their rows and store 64 bytes of a row together.
+        uint32_t to[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) to[x] = static_cast<uint32_t>(out_row((row & ~3) + x));  // T * H < 2^31
+        // v[4 x ..] goes in as piece x of this lane's row and comes out as this lane's piece of row x
+        auto exchange = [&](uint32_t (&v)[16]) {
+#pragma unroll
+          for (int bit = 1; bit <= 2; bit *= 2) {
+            const bool up = (lane & bit) != 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (x & bit) continue;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[4 * x + c] : v[4 * (x + bit) + c], bit);
+                if (up) v[4 * x + c] = got;
+                else v[4 * (x + bit) + c] = got;
+              }
+            }
+          }
+        };
 #pragma unroll 1
         for (int i = 4 * half; i < 4 * half + 4; ++i) {
           float o[32];
@@ -891,26 +923,34 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             for (int j = max(lo, w.it.lo0); j < min(w.it.lo1, min(hi, w.it.hi0)); ++j)
               if (j >= first) back(j);
           }
-          if (row < w.it.rows) {
-            if (whole) {
-              uint4* y = reinterpret_cast<uint4*>(out + orow * kHeadDim + 32 * i);
+          __syncwarp();
+          uint32_t v[16];
+          if (whole) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                y[c] = make_uint4(pack_bf16(o[8 * c] * inv, o[8 * c + 1] * inv),
-                                  pack_bf16(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
-                                  pack_bf16(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
-                                  pack_bf16(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
-            } else {
-              float4* y = reinterpret_cast<float4*>(part + static_cast<int64_t>(slot) * kPartFloats + row * kHeadDim +
-                                                    32 * i);
+            for (int c = 0; c < 16; ++c) v[c] = pack_bf16(o[2 * c] * inv, o[2 * c + 1] * inv);
+            exchange(v);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) y[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int x = 0; x < 4; ++x)
+              if ((row & ~3) + x < w.it.rows)
+                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(to[x]) * kHeadDim + 32 * i + 8 * (lane & 3)) =
+                    make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+          } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(o[16 * g + c]);
+              exchange(v);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if ((row & ~3) + x < w.it.rows)
+                  *reinterpret_cast<uint4*>(part + static_cast<int64_t>(slot) * kPartFloats + ((row & ~3) + x) * kHeadDim +
+                                            32 * i + 16 * g + 4 * (lane & 3)) =
+                      make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
             }
           }
-          __syncwarp();
         }
         if (half == 0 && row < w.it.rows) {
-          if (whole) lse[orow] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
+          if (whole) lse[out_row(row)] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
           else part_ml[slot * kRows + row] = make_float2(m, total);
         }
       }
