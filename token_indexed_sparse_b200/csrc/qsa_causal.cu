@@ -41,6 +41,7 @@
 #include "qsa_cache.cuh"
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
+#include "qsa_launch.cuh"
 
 namespace qsa {
 namespace {
@@ -670,15 +671,16 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     do {
       if (w.k > 0) ok = warp_wait(bar(kBQEmpty), (w.k - 1) & 1, abort_flag);
       if (!ok) break;
-      // a 512-byte row an instruction; rows past the last are zeros up to the 32 of a softmax warp
-      const int n = min(kRows, (w.it.rows + 31) & ~31), r0 = w.i * kRows;
+      // a 512-byte row an instruction; rows past the last are zeros, whose products draw less power than
+      // leftovers (a decode step of 12 rows kept up for a second: 315 us against 327)
+      const int r0 = w.i * kRows;
       int h = r0 % kHeadsPerGroup;
       const __nv_bfloat16* src = q + ((static_cast<int64_t>(w.s.start) + r0 / kHeadsPerGroup) * H +
                                       w.g * kHeadsPerGroup + h) * kHeadDim + lane * 8;
       const int64_t to_next_token = static_cast<int64_t>(H - kHeadsPerGroup + 1) * kHeadDim;
       const uint32_t dst = sb + (lane >> 3) * (kRows * 128);
 #pragma unroll 4
-      for (int r = 0; r < n; ++r) {
+      for (int r = 0; r < kRows; ++r) {
         cp_async16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src, r < w.it.rows);
         if (++h == kHeadsPerGroup) {
           h = 0;
@@ -978,15 +980,16 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
 // many rows has few parts: a warp takes a row (row 16 y + warp of block y).  One with many parts (few
 // rows, a long cache): a block takes row y, y + 12, ..., its warps a sixteenth of the parts each,
 // added in order.  Also gathers the ranges' status into the call's.
-constexpr int kJoinWarps = 16, kJoinBlocks = kHeadsPerGroup;
+constexpr int kJoinWarps = 16, kJoinBlocks = kHeadsPerGroup, kBatch = 5;
 static_assert(kJoinWarps * kJoinBlocks >= kRows, "a warp per row");
 __global__ void __launch_bounds__(kJoinWarps * 32)
 causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ part_ml, const Cont* __restrict__ cont,
                    int G, int* __restrict__ status, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   __shared__ float sO[kJoinWarps][kHeadDim];
-  __shared__ float sL[kJoinWarps];
+  __shared__ float2 sMl[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x;
+  after_previous();
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     int bad = 0;
     for (int c = threadIdx.x; c < static_cast<int>(gridDim.x); c += blockDim.x) bad |= cont[c].status;
@@ -997,30 +1000,43 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
   if (ct.rows == 0) return;
   const int n = ct.c_last - c0 + 1;  // part 0: slot (c0, 1), part i: slot (c0 + i, 0)
   auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
-  // this warp's sums (dims 8 lane on) of parts [a, z) of row r against the row's maximum m
-  float o[8], l;
-  auto add = [&](int r, int a, int z, float m) {
+  // this warp's sums (dims 8 lane on) of parts [a, z) of row r, against their largest maximum m
+  float o[8], l, m;
+  auto add = [&](int r, int a, int z) {
     l = 0.f;
+    m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.f;
-#pragma unroll 8
-    for (int i = a; i < z; ++i) {
-      const float2 ml = part_ml[slot(i) * kRows + r];
-      const float4* p = reinterpret_cast<const float4*>(part + static_cast<int64_t>(slot(i)) * kPartFloats + r * kHeadDim) +
-                        2 * lane;
-      const float4 u = p[0], v = p[1];
-      const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - m);  // sums without a maximum are zeros or NaN
-      l += ml.y * f;
-      o[0] += u.x * f, o[1] += u.y * f, o[2] += u.z * f, o[3] += u.w * f;
-      o[4] += v.x * f, o[5] += v.y * f, o[6] += v.z * f, o[7] += v.w * f;
-    }
-  };
-  auto max_of = [&](int r) {
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, part_ml[slot(i) * kRows + r].x);
+    for (; a < z; a += kBatch) {  // a batch's reads in flight together
+      float2 ml[kBatch];
+      float4 u[kBatch], v[kBatch];
+      float top = m;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    return m;
+      for (int i = 0; i < kBatch; ++i) {
+        if (a + i >= z) continue;
+        ml[i] = part_ml[slot(a + i) * kRows + r];
+        const float4* p =
+            reinterpret_cast<const float4*>(part + static_cast<int64_t>(slot(a + i)) * kPartFloats + r * kHeadDim) + 2 * lane;
+        u[i] = p[0];
+        v[i] = p[1];
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (a + i < z) top = fmaxf(top, ml[i].x);
+      const float g = m == top ? 1.f : exp2f(m - top);
+      m = top;
+      l *= g;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] *= g;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (a + i >= z) continue;
+        const float f = ml[i].x == -INFINITY ? 1.f : exp2f(ml[i].x - m);  // sums without a maximum are zeros or NaN
+        l += ml[i].y * f;
+        o[0] += u[i].x * f, o[1] += u[i].y * f, o[2] += u[i].z * f, o[3] += u[i].w * f;
+        o[4] += v[i].x * f, o[5] += v[i].y * f, o[6] += v[i].z * f, o[7] += v[i].w * f;
+      }
+    }
   };
   auto row_of = [&](int r) {
     const int f = ct.first + r;
@@ -1030,8 +1046,7 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
   if (n <= kJoinWarps) {
     const int r = kJoinWarps * blockIdx.y + warp;
     if (r >= ct.rows) return;
-    const float m = max_of(r);
-    add(r, 0, n, m);
+    add(r, 0, n);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t row = row_of(r);
     *reinterpret_cast<uint4*>(out + row * kHeadDim + 8 * lane) =
@@ -1041,23 +1056,25 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
     return;
   }
   for (int r = blockIdx.y; r < ct.rows; r += kJoinBlocks) {
-    const float m = max_of(r);
-    add(r, n * warp / kJoinWarps, n * (warp + 1) / kJoinWarps, m);
+    add(r, n * warp / kJoinWarps, n * (warp + 1) / kJoinWarps);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) sO[warp][8 * lane + i] = o[i];
-    if (lane == 0) sL[warp] = l;
+    if (lane == 0) sMl[warp] = make_float2(m, l);
     __syncthreads();
     if (threadIdx.x >= kHeadDim) continue;
-    float total = 0.f, y = 0.f;
+    float top = -INFINITY, total = 0.f, y = 0.f;
+#pragma unroll
+    for (int x = 0; x < kJoinWarps; ++x) top = fmaxf(top, sMl[x].x);
 #pragma unroll
     for (int x = 0; x < kJoinWarps; ++x) {
-      total += sL[x];
-      y += sO[x][threadIdx.x];
+      const float f = sMl[x].x == -INFINITY ? 1.f : exp2f(sMl[x].x - top);
+      total += sMl[x].y * f;
+      y += sO[x][threadIdx.x] * f;
     }
     const int64_t row = row_of(r);
     out[row * kHeadDim + threadIdx.x] = __float2bfloat16_rn(total == 0.f ? 0.f : y / total);
-    if (threadIdx.x == 0) lse[row] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
+    if (threadIdx.x == 0) lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
   }
 }
 
@@ -1105,9 +1122,9 @@ cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* 
                                               scale * kLog2e, part, ml, cont, static_cast<__nv_bfloat16*>(out), lse);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  causal_join_kernel<<<dim3(grid, kJoinBlocks), kJoinWarps * 32, 0, s>>>(part, ml, cont, G, status,
-                                                                      static_cast<__nv_bfloat16*>(out), lse);
-  return cudaGetLastError();
+  return launch_after(causal_join_kernel, dim3(grid, kJoinBlocks), kJoinWarps * 32, 0, s,
+                      static_cast<const float*>(part), static_cast<const float2*>(ml), static_cast<const Cont*>(cont), G,
+                      status, static_cast<__nv_bfloat16*>(out), lse);
 }
 
 }  // namespace qsa

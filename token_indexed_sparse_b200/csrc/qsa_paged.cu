@@ -12,6 +12,7 @@
 // part order (bit for bit reproducible).
 #include "qsa_internal.h"
 #include "qsa_device.cuh"
+#include "qsa_launch.cuh"
 
 namespace qsa {
 namespace {
@@ -59,6 +60,7 @@ paged_rows_kernel(const int32_t* __restrict__ routes, CacheView cache, int n_sel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t* ids = routes + t * n_sel;
   const int i0 = PER * tid;
+  next_may_start();
   int id[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) id[j] = i0 + j < n_sel ? __ldg(ids + i0 + j) : -1;
@@ -136,6 +138,8 @@ paged_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restric
   float* sSum = reinterpret_cast<float*>(smem + kOffSum);
   int* sJump = reinterpret_cast<int*>(smem + kOffJump);
   if (tid < 32) reinterpret_cast<uint4*>(smem + kOffZero)[tid] = make_uint4(0, 0, 0, 0);
+  next_may_start();
+  after_previous();
 
   // The chunk to issue next: item (t, g, split), keys [key0, key_end) of its row's list.
   unsigned it = blockIdx.x;
@@ -400,6 +404,7 @@ paged_join_kernel(const float* __restrict__ partial, const int32_t* __restrict__
   const int h = MANY ? blockIdx.x - item * kHeadsPerGroup : warp;
   const float* base = partial + static_cast<int64_t>(item) * splits * kPartFloats;
   const float* ml = base + kHeadsPerGroup * kPartRow + 2 * h;
+  after_previous();
   const bool none = __ldg(row_cnt + item / G) < 0;
   float m = -INFINITY;
   for (int i = lane; i < splits; i += 32) m = fmaxf(m, ml[static_cast<int64_t>(i) * kPartFloats]);
@@ -495,19 +500,17 @@ cudaError_t launch_paged_forward(const void* q, const void* k_pages, const void*
   if (e != cudaSuccess) return e;
   const int64_t n_items = T * G * splits;
   const int64_t slots = static_cast<int64_t>(kCps) * sm_count();
-  paged_kernel<<<static_cast<unsigned>(n_items < slots ? n_items : slots), kThreads, kSmem, s>>>(
-      static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k_pages),
-      static_cast<const __nv_bfloat16*>(v_pages), row_cnt, row_cols, n_sel, static_cast<unsigned>(n_items), G, splits,
-      scale * kLog2e, static_cast<float*>(partial), static_cast<__nv_bfloat16*>(out), lse);
-  e = cudaGetLastError();
+  e = launch_after(paged_kernel, dim3(static_cast<unsigned>(n_items < slots ? n_items : slots)), kThreads, kSmem, s,
+                   static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k_pages),
+                   static_cast<const __nv_bfloat16*>(v_pages), row_cnt, row_cols, n_sel,
+                   static_cast<unsigned>(n_items), G, splits, scale * kLog2e, static_cast<float*>(partial),
+                   static_cast<__nv_bfloat16*>(out), lse);
   if (e != cudaSuccess || splits == 1) return e;
-  if (splits > kManyParts)
-    paged_join_kernel<true><<<static_cast<unsigned>(T * G * kHeadsPerGroup), 256, 0, s>>>(
-        static_cast<const float*>(partial), row_cnt, G, splits, static_cast<__nv_bfloat16*>(out), lse);
-  else
-    paged_join_kernel<false><<<static_cast<unsigned>(T * G), kHeadsPerGroup * 32, 0, s>>>(
-        static_cast<const float*>(partial), row_cnt, G, splits, static_cast<__nv_bfloat16*>(out), lse);
-  return cudaGetLastError();
+  const bool many = splits > kManyParts;
+  return launch_after(many ? paged_join_kernel<true> : paged_join_kernel<false>,
+                      dim3(static_cast<unsigned>(T * G * (many ? kHeadsPerGroup : 1))),
+                      many ? 256 : kHeadsPerGroup * 32, 0, s, static_cast<const float*>(partial), row_cnt, G, splits,
+                      static_cast<__nv_bfloat16*>(out), lse);
 }
 
 }  // namespace qsa
