@@ -24,13 +24,17 @@ struct CacheView {
 };
 
 // The sequence of packed row t (the last one that starts at or before t, so
-// sequences without new tokens are passed over), or -1 for a row of none.
+// sequences without new tokens are passed over), or -1 for a row of none.  All
+// lanes of the warp search together, 32 offsets a step (log2(B) reads one after
+// another cost a decode step microseconds).
 __device__ __forceinline__ int cache_seq(const CacheView& c, int64_t t) {
-  int lo = 0, hi = c.B;  // cu_q[lo] <= t is known only after the search
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = c.B;  // in [lo, hi); cu_q[lo] <= t is known only after the search
   while (hi - lo > 1) {
-    const int mid = lo + ((hi - lo) >> 1);
-    if (__ldg(c.cu_q + mid) <= t) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const bool before = lane == 0 || (i < hi && __ldg(c.cu_q + i) <= t);
+    lo += (31 - __clz(static_cast<int>(__ballot_sync(0xffffffffu, before)))) * step;
+    hi = min(hi, lo + step);
   }
   return __ldg(c.cu_q + lo) <= t && t < __ldg(c.cu_q + lo + 1) ? lo : -1;
 }

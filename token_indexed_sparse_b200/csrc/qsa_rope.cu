@@ -13,12 +13,16 @@
 // fraction of a turn with no range reduction, and its top 32 bits as half-turns
 // go to sincospi (error about 1e-7 of a radian).
 //
-// Bound by memory: every 16-byte piece is read and written once.  A block takes
-// kTok tokens; each thread first issues the loads of its pieces, then computes one
-// (token, pair) cosine and sine into shared memory for all heads, then rotates
-// in FP32 and rounds once.  A thread's unit is two 16-byte pieces of one head
-// that hold eight whole pairs in either layout, so both layouts move whole
-// 16-byte pieces.
+// Bound by memory: every 16-byte piece is read and written once, past the caches
+// (evict-first; with default stores the append of 16 k tokens took 94 us, not 91).
+// A block takes a few tokens, as many as give each thread its units (four, two in
+// the append; fewer leave too little in flight: 12 + 1 heads of 16384 tokens took
+// 47 us with two tokens a block, 42 with four).  Each thread first issues the loads
+// of its units, then the block computes the cosines and sines of its (token, pair)s
+// into shared memory for all heads, then each thread rotates its units in FP32 and
+// rounds once.  A unit is two 16-byte pieces of one head that hold eight whole pairs
+// in either layout.  26 heads of 32768 tokens: 138 us, 6.3 TB/s (133 us at the rate
+// of a plain copy).
 #include "qsa_cache.cuh"
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
@@ -27,9 +31,9 @@ namespace qsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kTok = 2;                          // tokens per block
+constexpr int kMaxTok = 8;                       // tokens per block at most
 constexpr int kUnits = kHeadDim / 16;            // two-piece units per head
-constexpr int kAhead = 4;                        // units whose loads a thread holds
+constexpr int kAhead = 4, kAppendAhead = 2;      // units whose loads a thread holds
 constexpr int kCsUnit = 9;                       // a unit's eight (cos, sin) and one of padding: no bank conflicts
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
@@ -79,50 +83,61 @@ __device__ __forceinline__ const uint4* piece(const HeadRows& x, int64_t t, int 
   return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.p) + t * x.ts + h * x.hs);
 }
 
-// Rotates q (H heads) and k (G heads) of T tokens.
+// cos and sin (times m) of the block's tokens and pairs.
+template <class Pos>
+__device__ __forceinline__ void fill_turns(float2 (*cs)[kUnits * kCsUnit], const double* inv_freq, Pos pos, int n_tok,
+                                           int rot, float m) {
+  const int pairs = rot / 2;
+  for (int i = threadIdx.x; i < n_tok * pairs; i += kRopeThreads) {
+    const int tok = i / pairs, f = i - tok * pairs;
+    cs[tok][(f >> 3) * kCsUnit + (f & 7)] = turned(__ldg(inv_freq + f), pos(tok), m);
+  }
+}
+
+// A block's units, four per thread and round: unit u is unit j of head h of token tok.
+struct Unit {
+  int tok, h, j;
+};
+__device__ __forceinline__ Unit unit_at(int u, int heads) {
+  const int r = u / kUnits, tok = r / heads;
+  return {tok, r - tok * heads, u % kUnits};
+}
+
+// Rotates q (H heads) and k (G heads) of T tokens, n_blk a block.
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(HeadRows q, HeadRows k, HeadRows qo, HeadRows ko, const int32_t* __restrict__ positions,
-            const double* __restrict__ inv_freq, int64_t T, int H, int G, int rot, bool inter, float m, float sign) {
-  __shared__ float2 cs[kTok][kUnits * kCsUnit];
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok;
-  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kTok), T - t0));
+            const double* __restrict__ inv_freq, int64_t T, int H, int G, int rot, bool inter, float m, float sign,
+            int n_blk) {
+  __shared__ float2 cs[kMaxTok][kUnits * kCsUnit];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * n_blk;
+  const int n_tok = static_cast<int>(min(static_cast<int64_t>(n_blk), T - t0));
   const int units = n_tok * (H + G) * kUnits;
   for (int u0 = 0; u0 < units; u0 += kAhead * kRopeThreads) {
     uint4 a[kAhead], b[kAhead];
-    // unit u: token u / ((H + G) kUnits), head, unit of the head
-    auto where = [&](int u, int& tok, int& h, int& j) {
-      j = u % kUnits;
-      const int r = u / kUnits;
-      tok = r / (H + G);
-      h = r - tok * (H + G);
-    };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int u = u0 + i * kRopeThreads + threadIdx.x;
       if (u >= units) continue;
-      int tok, h, j;
-      where(u, tok, h, j);
-      const uint4* x = h < H ? piece(q, t0 + tok, h) : piece(k, t0 + tok, h - H);
-      const int2 pc = unit_pieces(j, rot, inter);
-      a[i] = x[pc.x];
-      b[i] = x[pc.y];
+      const Unit x = unit_at(u, H + G);
+      const uint4* src = x.h < H ? piece(q, t0 + x.tok, x.h) : piece(k, t0 + x.tok, x.h - H);
+      const int2 pc = unit_pieces(x.j, rot, inter);
+      a[i] = __ldcs(src + pc.x);
+      b[i] = __ldcs(src + pc.y);
     }
     if (u0 == 0) {
-      const int tok = threadIdx.x >> 7, f = threadIdx.x & 127;
-      if (tok < n_tok && f < rot / 2) cs[tok][(f >> 3) * kCsUnit + (f & 7)] = turned(__ldg(inv_freq + f), __ldg(positions + t0 + tok), m);
+      fill_turns(cs, inv_freq, [&](int tok) { return static_cast<int64_t>(__ldg(positions + t0 + tok)); }, n_tok, rot, m);
       __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int u = u0 + i * kRopeThreads + threadIdx.x;
       if (u >= units) continue;
-      int tok, h, j;
-      where(u, tok, h, j);
-      if (j < rot / 16) rotate_unit(a[i], b[i], cs[tok] + kCsUnit * j, inter, sign);
-      uint4* y = const_cast<uint4*>(h < H ? piece(qo, t0 + tok, h) : piece(ko, t0 + tok, h - H));
-      const int2 pc = unit_pieces(j, rot, inter);
-      y[pc.x] = a[i];
-      y[pc.y] = b[i];
+      const Unit x = unit_at(u, H + G);
+      if (x.j < rot / 16) rotate_unit(a[i], b[i], cs[x.tok] + kCsUnit * x.j, inter, sign);
+      uint4* dst = const_cast<uint4*>(x.h < H ? piece(qo, t0 + x.tok, x.h) : piece(ko, t0 + x.tok, x.h - H));
+      const int2 pc = unit_pieces(x.j, rot, inter);
+      __stcs(dst + pc.x, a[i]);
+      __stcs(dst + pc.y, b[i]);
     }
   }
 }
@@ -130,71 +145,72 @@ rope_kernel(HeadRows q, HeadRows k, HeadRows qo, HeadRows ko, const int32_t* __r
 // Writes a packed batch's new K (rotated) and V rows into their pages, and the
 // rotated q rows (when nq > 0; nq = H, or 0 without q) to qo.  Rows of no sequence
 // are left alone; a row whose position has no page gets its q but no K/V row.
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 6)
 append_kernel(HeadRows q, HeadRows k, HeadRows v, HeadRows qo, __nv_bfloat16* __restrict__ k_pages,
               __nv_bfloat16* __restrict__ v_pages, CacheView c, const double* __restrict__ inv_freq, int64_t T, int nq,
-              int G, int rot, bool inter, float m) {
-  __shared__ float2 cs[kTok][kUnits * kCsUnit];
-  __shared__ int64_t s_pos[kTok];
-  __shared__ int s_row[kTok];  // pool row, -1 without a page, -2 for a row of no sequence
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok;
-  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kTok), T - t0));
-  const int heads = nq + 2 * G;
+              int G, int rot, bool inter, float m, int n_blk) {
+  __shared__ float2 cs[kMaxTok][kUnits * kCsUnit];
+  __shared__ int64_t s_pos[kMaxTok];
+  __shared__ int s_row[kMaxTok];  // pool row, -1 without a page, -2 for a row of no sequence
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * n_blk;
+  const int n_tok = static_cast<int>(min(static_cast<int64_t>(n_blk), T - t0));
+  const int heads = nq + 2 * G;  // in the order q, k, v
   const int units = n_tok * heads * kUnits;
-  for (int u0 = 0; u0 < units; u0 += kAhead * kRopeThreads) {
-    uint4 a[kAhead], b[kAhead];
-    auto where = [&](int u, int& tok, int& h, int& j) {  // heads in the order q, k, v
-      j = u % kUnits;
-      const int r = u / kUnits;
-      tok = r / heads;
-      h = r - tok * heads;
-    };
-    auto pieces = [&](int h, int j) { return unit_pieces(j, h < nq + G ? rot : 0, inter); };
+  for (int u0 = 0; u0 < units; u0 += kAppendAhead * kRopeThreads) {
+    uint4 a[kAppendAhead], b[kAppendAhead];
+    auto pieces = [&](const Unit& x) { return unit_pieces(x.j, x.h < nq + G ? rot : 0, inter); };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kAppendAhead; ++i) {
       const int u = u0 + i * kRopeThreads + threadIdx.x;
       if (u >= units) continue;
-      int tok, h, j;
-      where(u, tok, h, j);
-      const uint4* x = h < nq ? piece(q, t0 + tok, h)
-                              : (h < nq + G ? piece(k, t0 + tok, h - nq) : piece(v, t0 + tok, h - nq - G));
-      const int2 pc = pieces(h, j);
-      a[i] = x[pc.x];
-      b[i] = x[pc.y];
+      const Unit x = unit_at(u, heads);
+      const uint4* src = x.h < nq ? piece(q, t0 + x.tok, x.h)
+                                  : (x.h < nq + G ? piece(k, t0 + x.tok, x.h - nq) : piece(v, t0 + x.tok, x.h - nq - G));
+      const int2 pc = pieces(x);
+      a[i] = __ldcs(src + pc.x);
+      b[i] = __ldcs(src + pc.y);
     }
     if (u0 == 0) {
-      if (threadIdx.x < n_tok) {
-        const int seq = cache_seq(c, t0 + threadIdx.x);
-        const int64_t pos = seq < 0 ? 0 : cache_pos(c, seq, t0 + threadIdx.x);
-        s_pos[threadIdx.x] = pos;
-        s_row[threadIdx.x] = seq < 0 ? -2 : cache_row(c, seq, pos);
+      const int tok = threadIdx.x >> 5;  // a warp per token looks its place up
+      static_assert(kMaxTok <= kRopeThreads / 32, "a warp per token");
+      if (tok < n_tok) {
+        const int seq = cache_seq(c, t0 + tok);
+        const int64_t pos = seq < 0 ? 0 : cache_pos(c, seq, t0 + tok);
+        s_pos[tok] = pos;
+        s_row[tok] = seq < 0 ? -2 : cache_row(c, seq, pos);
       }
       __syncthreads();
-      const int tok = threadIdx.x >> 7, f = threadIdx.x & 127;
-      if (tok < n_tok && f < rot / 2) cs[tok][(f >> 3) * kCsUnit + (f & 7)] = turned(__ldg(inv_freq + f), s_pos[tok], m);
+      fill_turns(cs, inv_freq, [&](int tok) { return s_pos[tok]; }, n_tok, rot, m);
       __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kAppendAhead; ++i) {
       const int u = u0 + i * kRopeThreads + threadIdx.x;
       if (u >= units) continue;
-      int tok, h, j;
-      where(u, tok, h, j);
-      const int row = s_row[tok];
-      if (row < (h < nq ? -1 : 0)) continue;
-      if (j < rot / 16 && h < nq + G) rotate_unit(a[i], b[i], cs[tok] + kCsUnit * j, inter, 1.f);
-      uint4* y;
-      if (h < nq) {
-        y = const_cast<uint4*>(piece(qo, t0 + tok, h));
+      const Unit x = unit_at(u, heads);
+      const int row = s_row[x.tok];
+      if (row < (x.h < nq ? -1 : 0)) continue;
+      if (x.j < rot / 16 && x.h < nq + G) rotate_unit(a[i], b[i], cs[x.tok] + kCsUnit * x.j, inter, 1.f);
+      uint4* dst;
+      if (x.h < nq) {
+        dst = const_cast<uint4*>(piece(qo, t0 + x.tok, x.h));
       } else {
-        const int g = h < nq + G ? h - nq : h - nq - G;
-        y = reinterpret_cast<uint4*>((h < nq + G ? k_pages : v_pages) + (static_cast<int64_t>(row) * G + g) * kHeadDim);
+        const int g = x.h < nq + G ? x.h - nq : x.h - nq - G;
+        dst = reinterpret_cast<uint4*>((x.h < nq + G ? k_pages : v_pages) + (static_cast<int64_t>(row) * G + g) * kHeadDim);
       }
-      const int2 pc = pieces(h, j);
-      y[pc.x] = a[i];
-      y[pc.y] = b[i];
+      const int2 pc = pieces(x);
+      __stcs(dst + pc.x, a[i]);
+      __stcs(dst + pc.y, b[i]);
     }
   }
+}
+
+// Tokens per block: `ahead` units a thread, but one token where there are few (a block per SM and more).
+int tokens_per_block(int64_t T, int heads, int ahead) {
+  int n = ahead * kRopeThreads / (heads * kUnits);
+  n = n < 1 ? 1 : (n > kMaxTok ? kMaxTok : n);
+  while (n > 1 && (T + n - 1) / n < 4 * sm_count()) n /= 2;
+  return n;
 }
 
 }  // namespace
@@ -202,17 +218,19 @@ append_kernel(HeadRows q, HeadRows k, HeadRows v, HeadRows qo, __nv_bfloat16* __
 cudaError_t launch_rope(const HeadRows& q, const HeadRows& k, const HeadRows& qo, const HeadRows& ko,
                         const int32_t* positions, const double* inv_freq, int64_t T, int H, int G, int rot, bool inter,
                         float m, bool backward, cudaStream_t s) {
-  rope_kernel<<<static_cast<unsigned>((T + kTok - 1) / kTok), kRopeThreads, 0, s>>>(
-      q, k, qo, ko, positions, inv_freq, T, H, G, rot, inter, m, backward ? -1.f : 1.f);
+  const int n = tokens_per_block(T, H + G, kAhead);
+  rope_kernel<<<static_cast<unsigned>((T + n - 1) / n), kRopeThreads, 0, s>>>(
+      q, k, qo, ko, positions, inv_freq, T, H, G, rot, inter, m, backward ? -1.f : 1.f, n);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_append(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& qo,
                                 void* k_pages, void* v_pages, const CacheView& c, const double* inv_freq, int64_t T,
                                 int nq, int G, int rot, bool inter, float m, cudaStream_t s) {
-  append_kernel<<<static_cast<unsigned>((T + kTok - 1) / kTok), kRopeThreads, 0, s>>>(
+  const int n = tokens_per_block(T, nq + 2 * G, kAppendAhead);
+  append_kernel<<<static_cast<unsigned>((T + n - 1) / n), kRopeThreads, 0, s>>>(
       q, k, v, qo, static_cast<__nv_bfloat16*>(k_pages), static_cast<__nv_bfloat16*>(v_pages), c, inv_freq, T, nq, G,
-      rot, inter, m);
+      rot, inter, m, n);
   return cudaGetLastError();
 }
 
