@@ -73,9 +73,12 @@ constexpr int kMinTiles = 2;                   // fewer tiles than this are not 
 constexpr int kMaxCtas = 148;
 constexpr int kPartFloats = kRows * kHeadDim;  // FP32 sums of a part
 // kind::f16, FP32 accumulate, BF16: S (both K-major, N 128) and O (B MN-major, N 256)
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10);
 constexpr uint32_t kIdescS = kIdesc | ((128u >> 3) << 17);
 constexpr uint32_t kIdescO = kIdesc | (1u << 16) | ((256u >> 3) << 17);
+// M, in the instruction descriptor.  A tile of one token (12 rows) takes M 64: its first 16 rows lie in
+// the same lanes, the time is the same, the power is not.
+__device__ __forceinline__ uint32_t idesc_m(int rows) { return (rows <= 16 ? 64u >> 4 : 128u >> 4) << 24; }
 
 struct Args {
   CacheView c;
@@ -254,18 +257,18 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr, int run) {
   return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(run * 128 >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdescS), "r"(accumulate)
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(kIdescO), "r"(accumulate)
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -579,6 +582,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         do {
           ok = wait(kBQFull, w.k & 1);
           const int n = w.x1 - w.x0;
+          const uint32_t idesc = kIdescS | idesc_m(w.it.rows);
 #pragma unroll 1
           for (int y = 0; y < n && ok; ++y, ++tau) {
             const uint32_t s = tmem + kColS + 128 * (tau & 1);
@@ -605,7 +609,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 mma_ss(s, qd + (i >> 2) * (kRows * 128 >> 4) + 2 * (i & 3), kd + (i >> 2) * (kSubBytes >> 4) + 2 * (i & 3),
-                       i > 0 || u > 0);
+                       idesc, i > 0 || u > 0);
               commit(bar(kBEmpty + ring.slot));
               ring.step();
             }
@@ -621,6 +625,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         do {
           const int n = w.x1 - w.x0;
           bool summing = false;       // the item's first product starts its sums
+          const uint32_t idesc = kIdescO | idesc_m(w.it.rows);
           ring.step(n > 1 ? 4 : 2);   // K of the first two tiles
 #pragma unroll 1
           for (int y = 0; y < n && ok; ++y, ++tau) {
@@ -645,7 +650,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               for (int i = 0; i < 4; ++i) {  // 16 keys: a run, or half of one
                 if (!(steps >> (4 * u + i) & 1)) continue;
                 mma_ts(tmem, p + 64 * u + 8 * i,
-                       vd + (run == 16 ? i * (8192 >> 4) : (i >> 1) * (kSubBytes >> 4) + (i & 1) * (2048 >> 4)), summing);
+                       vd + (run == 16 ? i * (8192 >> 4) : (i >> 1) * (kSubBytes >> 4) + (i & 1) * (2048 >> 4)), idesc, summing);
                 summing = true;
               }
               commit(bar(kBEmpty + ring.slot));
