@@ -344,6 +344,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// Two FP32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
 // Bounded wait that also gives up once another role has.
@@ -772,7 +786,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           uint32_t pk[32];
           const float m_old = m;
           for (bool again = false;; again = true) {
-            float s[64], l0 = 0.f, l1 = 0.f;
+            float s[64];
+            float2 ls = make_float2(0.f, 0.f);
             tmem_ld64(s_addr, s);
             if (edge) {
               const uint32_t v0 = vis(2 * half), v1 = vis(2 * half + 1);
@@ -792,13 +807,12 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
-              const float p0 = exp2_fast(fmaf(s[c], scale_log2, -base));
-              const float p1 = exp2_fast(fmaf(s[c + 1], scale_log2, -base));
-              l0 += p0;
-              l1 += p1;
-              pk[c >> 1] = pack_bf16(p0, p1);
+              const float2 x = fma2(make_float2(s[c], s[c + 1]), make_float2(scale_log2, scale_log2), make_float2(-base, -base));
+              const float2 p = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+              ls = add2(ls, p);
+              pk[c >> 1] = pack_bf16(p.x, p.y);
             }
-            sum = l0 + l1;
+            sum = ls.x + ls.y;
             if (again || y == 0) break;
             top = fmaxf(top, other());
             if (top > m + kLag) m = top;
