@@ -155,38 +155,36 @@ __device__ __forceinline__ bool step_seen(const Item& it, int first, int key) {
   return key == 0 || key < first || (key < it.hi1 && key + 16 > it.lo0);
 }
 
-// The CTA's walk: pieces (item, tiles [x0, x1)) of its range.  Every role walks alone.
+// The CTA's walk: pieces (item, tiles [x0, x1)) of its range.  Every role walks alone:
+//   Walk w(...); while (w.take(a)) { ...; }
 struct Walk {
   int b, i, g, x0, x1;
   int64_t left;   // tiles after this piece
   int k;          // piece counter
   Seq s;
   Item it;
-  __device__ __forceinline__ void take(const Args& a) {
+  __device__ __forceinline__ Walk(const Args& a, const int* start, int64_t tiles)
+      : b(start[0]), i(start[1]), g(start[2]), x0(0), x1(start[3]), left(tiles), k(-1), s(seq_of(a, b)) {
+    it.n = 0;
+  }
+  __device__ __forceinline__ bool take(const Args& a) {  // the next piece (one site per role: it is much code)
+    if (left <= 0) return false;
+    if (++k == 0) {
+      x0 = x1;
+    } else {
+      x0 = 0;
+      if (++g == a.G) {
+        g = 0;
+        if (++i == query_tiles(s)) {
+          i = 0;
+          do s = seq_of(a, ++b);
+          while (s.n == 0);
+        }
+      }
+    }
     it = item_of(a, s, i);
     x1 = static_cast<int>(min(static_cast<int64_t>(it.n), x0 + left));
     left -= x1 - x0;
-  }
-  __device__ __forceinline__ void begin(const Args& a, const int* start, int64_t tiles) {
-    b = start[0], i = start[1], g = start[2], x0 = start[3];
-    left = tiles;
-    k = 0;
-    s = seq_of(a, b);
-    take(a);
-  }
-  __device__ __forceinline__ bool next(const Args& a) {
-    if (left <= 0) return false;
-    ++k;
-    x0 = 0;
-    if (++g == a.G) {
-      g = 0;
-      if (++i == query_tiles(s)) {
-        i = 0;
-        do s = seq_of(a, ++b);
-        while (s.n == 0);
-      }
-    }
-    take(a);
     return true;
   }
 };
@@ -308,6 +306,14 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
       : "r"(taddr) : "memory");
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
   asm volatile(
@@ -513,8 +519,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     Ring ring;
     uint32_t issued = 0;
     bool ok = true;
-    Walk w;
-    w.begin(a, start, tiles);
+    Walk w(a, start, tiles);
     // lane l holds the pool row of the first key of page l of a tile
     auto rows_of = [&](int x) {
       const int64_t j = static_cast<int64_t>(key_tile(w.it, x)) * kTileKeys + static_cast<int64_t>(lane) * page;
@@ -557,7 +562,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         ring.step();
       }
     };
-    do {
+    while (ok && w.take(a)) {
       int cur = rows_of(w.x0), prev = 0;
       for (int x = w.x0; x < w.x1 && ok; ++x) {
         const int ahead = x + 1 < w.x1 ? rows_of(x + 1) : 0;  // table reads a tile ahead of their use
@@ -567,7 +572,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         cur = ahead;
       }
       if (ok) load_v(prev);
-    } while (ok && w.next(a));
+    }
     if (!ok && lane == 0) {  // copies in flight end before the block does (bounded)
       Ring r = ring;
       for (uint32_t i = 0; i < min(issued, static_cast<uint32_t>(kUnits)); ++i) {
@@ -588,12 +593,11 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       Ring ring;
       bool ok = true;
       uint32_t tau = 0;  // tiles so far
-      Walk w;
-      w.begin(a, start, tiles);
+      Walk w(a, start, tiles);
       auto wait = [&](int i, uint32_t parity) { return wait_bar(bar(i), parity, abort_flag); };
       if (warp == kMmaS) {
         const uint64_t q_desc = desc_k_major(sb), k_desc = desc_k_major(sb + kOffRing);
-        do {
+        while (ok && w.take(a)) {
           ok = wait(kBQFull, w.k & 1);
           const int n = w.x1 - w.x0;
           const uint32_t idesc = kIdescS | idesc_m(w.it.rows);
@@ -632,11 +636,11 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           }
           if (ok) commit(bar(kBQEmpty));
           ring.step(2);               // V of the last tile
-        } while (ok && w.next(a));
+        }
       } else {
         const int run = v_run(a), first = first_keys(a);
         const uint64_t v_desc = desc_v(sb + kOffRing, run);
-        do {
+        while (ok && w.take(a)) {
           const int n = w.x1 - w.x0;
           bool summing = false;       // the item's first product starts its sums
           const uint32_t idesc = kIdescO | idesc_m(w.it.rows);
@@ -673,7 +677,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             commit(bar(kBPv + (tau & 1)));
             if (y + 2 < n) ring.step(2);  // K of tile y + 2
           }
-        } while (ok && w.next(a));
+        }
       }
       if (!ok) {  // the products in flight end before tensor memory is freed (bounded)
         const int i = kBDrain + (warp == kMmaO ? 1 : 0);
@@ -684,10 +688,9 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     __syncwarp();
   } else if (warp >= kLoader) {
     // ------------------------------------------------------------ Q rows
-    Walk w;
-    w.begin(a, start, tiles);
+    Walk w(a, start, tiles);
     bool ok = true;
-    do {
+    while (w.take(a)) {
       if (w.k > 0) ok = warp_wait(bar(kBQEmpty), (w.k - 1) & 1, abort_flag);
       if (!ok) break;
       // a 512-byte row an instruction; rows past the last are zeros, whose products draw less power than
@@ -712,7 +715,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       cp_async_wait<0>();
       fence_proxy_async();
       mbar_arrive(bar(kBQFull));
-    } while (w.next(a));
+    }
   } else {
     // ------------------------------------------------------------ softmax
     // Thread (half, row): keys 64 half .. 64 half + 63 of every tile.  Both halves of a tile at once
@@ -739,9 +742,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       bar_sync(1 + wq, 64);
       return sX[((ex++ & 1) * 2 + (half ^ 1)) * kRows + row];
     };
-    Walk w;
-    w.begin(a, start, tiles);
-    do {
+    Walk w(a, start, tiles);
+    while (w.take(a)) {
       const bool live = 32 * wq < w.it.rows;
       const int64_t r0 = static_cast<int64_t>(w.i) * kRows;
       const int64_t p = w.s.p0 + (r0 + row) / kHeadsPerGroup;
@@ -902,11 +904,29 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         const float inv = total == 0.f ? 0.f : 1.f / total;
         // Stores of whole rows by their threads would touch 32 lines each; so four lanes exchange the
         // 16-byte pieces of their rows and store 64 bytes of a row together.
-        uint32_t to[4];
+        // (One site for outputs and parts, rolled: this code runs once an item, out of a cold
+        // instruction cache.)
+        uint8_t* to[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) to[x] = static_cast<uint32_t>(out_row((row & ~3) + x));  // T * H < 2^31
-        // v[4 x ..] goes in as piece x of this lane's row and comes out as this lane's piece of row x
-        auto exchange = [&](uint32_t (&v)[16]) {
+        for (int x = 0; x < 4; ++x) {
+          const int r = (row & ~3) + x;
+          to[x] = whole ? reinterpret_cast<uint8_t*>(out + out_row(r) * kHeadDim)
+                        : reinterpret_cast<uint8_t*>(part + static_cast<int64_t>(slot) * kPartFloats + r * kHeadDim);
+          to[x] += 16 * (lane & 3);
+        }
+        const int pieces = whole ? 4 : 8;  // of 64 bytes, in this half's 128 dims
+#pragma unroll 1
+        for (int i = 0; i < pieces; ++i) {
+          // v[4 x ..] goes in as 16-byte piece x of this lane's row and comes out as this lane's piece of row x
+          uint32_t v[16];
+          if (whole) {
+            float o[32];
+            tmem_ld32(lanes + 128 * half + 32 * i, o);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = pack_bf16(o[2 * c] * inv, o[2 * c + 1] * inv);
+          } else {
+            tmem_ld16(lanes + 128 * half + 16 * i, v);
+          }
 #pragma unroll
           for (int bit = 1; bit <= 2; bit *= 2) {
             const bool up = (lane & bit) != 0;
@@ -921,52 +941,29 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
               }
             }
           }
-        };
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if ((row & ~3) + x < w.it.rows)
+              *reinterpret_cast<uint4*>(to[x] + 64 * (pieces * half + i)) =
+                  make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+        }
+        if (poisoned) {  // non-finite V elements taken out of the product, back where they are seen
+          __syncwarp();  // the row as its four lanes stored it
+          const int64_t at = out_row(row) * kHeadDim;
+          float* sums = part + static_cast<int64_t>(slot) * kPartFloats + row * kHeadDim;
 #pragma unroll 1
-        for (int i = 4 * half; i < 4 * half + 4; ++i) {
-          float o[32];
-          tmem_ld32(lanes + 32 * i, o);
-          if (poisoned && row < w.it.rows) {
-            // non-finite V elements taken out of the product, back where they are seen
-            const __nv_bfloat16* vp = v_pool + w.g * kHeadDim + 32 * i;
-            auto back = [&](int j) {
-              const int r = cache_row(a.c, w.b, j);
-              if (r < 0) return;
-              for (int c = 0; c < 32; ++c) {
-                const float x = __bfloat162float(vp[static_cast<int64_t>(r) * a.G * kHeadDim + c]);
-#pragma unroll
-                for (int d = 0; d < 32; ++d)
-                  if (d == c && !isfinite(x)) o[d] += x;
-              }
-            };
-            for (int j = w.it.hi0; j < hi; ++j)
-              if (j >= lo || j < first) back(j);
-            for (int j = max(lo, w.it.lo0); j < min(w.it.lo1, min(hi, w.it.hi0)); ++j)
-              if (j >= first) back(j);
-          }
-          __syncwarp();
-          uint32_t v[16];
-          if (whole) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = pack_bf16(o[2 * c] * inv, o[2 * c + 1] * inv);
-            exchange(v);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if ((row & ~3) + x < w.it.rows)
-                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(to[x]) * kHeadDim + 32 * i + 8 * (lane & 3)) =
-                    make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-          } else {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(o[16 * g + c]);
-              exchange(v);
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if ((row & ~3) + x < w.it.rows)
-                  *reinterpret_cast<uint4*>(part + static_cast<int64_t>(slot) * kPartFloats + ((row & ~3) + x) * kHeadDim +
-                                            32 * i + 16 * g + 4 * (lane & 3)) =
-                      make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+          for (int j = w.it.lo0; row < w.it.rows && j < hi; ++j) {
+            if (j >= w.it.lo1 && j < w.it.hi0) j = w.it.hi0;  // (seen by all: left in the product)
+            if (j >= hi || (j < lo && j >= first) || (j < first && j < w.it.hi0)) continue;
+            const int r = cache_row(a.c, w.b, j);
+            if (r < 0) continue;
+            const __nv_bfloat16* vr = v_pool + (static_cast<int64_t>(r) * a.G + w.g) * kHeadDim;
+#pragma unroll 1
+            for (int d = 128 * half; d < 128 * half + 128; ++d) {
+              const float x = __bfloat162float(vr[d]);
+              if (isfinite(x)) continue;
+              if (whole) out[at + d] = __float2bfloat16_rn(__bfloat162float(out[at + d]) + x);
+              else sums[d] += x;
             }
           }
         }
@@ -986,7 +983,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         cont[blockIdx.x] = ct;
       }
       fence_before();
-    } while (w.next(a));
+    }
   }
   fence_before();
   __syncthreads();
