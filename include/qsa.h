@@ -424,8 +424,8 @@ qsa_status_t qsa_forward_noalloc(const void* q, const void* k, const void* v, co
  *       row j % page_size of page block_table[b, j / page_size]
  *   kv_len [B] int32   : tokens that sequence b holds, its new ones included
  *   cu_q [B + 1] int32 : sequence b's new tokens are the packed rows
- *       [cu_q[b], cu_q[b + 1]) (ascending offsets, any of them empty); row t of
- *       them sits at position kv_len[b] - (cu_q[b + 1] - t)
+ *       [cu_q[b], cu_q[b + 1]) (offsets that do not descend, any of them empty);
+ *       row t of them sits at position kv_len[b] - (cu_q[b + 1] - t)
  * and T packed rows.  These arrays are read on the device only, so their values
  * are never errors: rows of no sequence (t < cu_q[0], or behind the last one)
  * are left as they were in every output; a position outside [0, max_pages *
@@ -453,7 +453,8 @@ qsa_status_t qsa_forward_noalloc(const void* q, const void* k, const void* v, co
  *   q, q_out [T, H, 256], k, k_out [T, G, 256] BF16 with element strides between
  *   tokens and heads (multiples of 8; dims contiguous; 16-byte aligned).  G = 0:
  *   no k.  Any H >= 1, G >= 0.  An output is its own input (same pointer and
- *   strides: in place) or overlaps it nowhere, and its rows do not overlap.
+ *   strides: in place) or overlaps it nowhere, and its rows do not overlap (both
+ *   checked); it overlaps nothing else that the call reads or writes.
  *   positions [T] int32 (any value); inv_freq [rotary_dim / 2] double, finite;
  *   rotary_dim a multiple of 16, at most 256 (else QSA_ERR_UNSUPPORTED);
  *   0 < mscale < inf.

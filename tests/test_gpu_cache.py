@@ -165,6 +165,8 @@ BATCHES = {
     "short_table": ([300, 90], [10, 60], 16, 1, {"max_pages": 4}),   # positions past the table have no page
     "short_len": ([3, 40], [8, 4], 16, 1, {}),                        # more new tokens than the cache holds
     "page256": ([513, 256], [20, 3], 256, 1, {}),
+    "page1024": ([1500], [9], 1024, 3, {}),
+    "negative": ([-3, 40, -2**31], [2, 7, 1], 16, 1, {}),             # a length below zero holds nothing
 }
 
 
@@ -190,12 +192,64 @@ def test_paged_forward(name, W):
     _check(c, *_attend(c, routes=r), routes=r)
 
 
-@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (13, 4), (64, 130), (200, 1), (10**9, 5)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (13, 4), (64, 130), (200, 1), (2**31 - 1, 2**31 - 1)])
 @pytest.mark.parametrize("name", BATCHES)
 def test_paged_causal(name, window, sinks):
     lens, news, page, G, more = BATCHES[name]
     c = _cache(lens, news, page, G, 12, **more)
     _check(c, *_attend(c, window=window, sinks=sinks), window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("W", [2049, 4097, 9001, 16384])
+def test_long_route_rows(W):
+    c = _cache([20000, 333], [2, 3], 64, 1, 21)
+    r = _routes(c, W, W)
+    r[1] = torch.randint(0, 50, (W,), generator=_gen(W), dtype=torch.int32)  # hardly anything but repeats
+    r[3] = 7
+    _check(c, *_attend(c, routes=r), routes=r)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5)])
+def test_items_cut_into_ranges(window, sinks):
+    # more key tiles than CTAs, items that end inside ranges and ranges inside items
+    c = _cache([2400, 130, 900], [330, 1, 77], 32, 2, 22)
+    _check(c, *_attend(c, window=window, sinks=sinks), window=window, sinks=sinks)
+
+
+def test_many_sequences_most_of_them_short_or_empty():
+    # more sequences and query tiles than the planning takes in one batch
+    g = _gen(23)
+    lens = torch.randint(0, 19, (1100,), generator=g).tolist()
+    news = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, 4, (1100,), generator=g))]
+    news[40] = lens[40] = 60
+    c = _cache(lens, news, 16, 1, 24, lead=1, behind=2)
+    _check(c, *_attend(c))
+    r = _routes(c, 12, 5)
+    _check(c, *_attend(c, routes=r), routes=r)
+
+
+def test_pools_past_32_bits():
+    # rows whose element offsets pass 2^32: pages at the end of 9 GB pools
+    page, G = 64, 2
+    n_pages = (2**32 // (G * 256) + 4096) // page
+    c = _cache([150], [60], page, G, 25)
+    d = {n: x.to(DEV) for n, x in c.items()}
+    kp, vp = (torch.empty(n_pages, page, G, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    last = torch.arange(n_pages - d["kp"].shape[0], n_pages, device=DEV)
+    kp[last], vp[last] = d["kp"], d["vp"]
+    table = torch.where(d["table"] >= 0, d["table"] + int(last[0]), -1).to(torch.int32)
+    where = (table, d["kv_len"], d["cu_q"])
+    out, lse = qsa.paged_causal(d["q"], kp, vp, *where, SCALE)
+    _check(c, out, lse)
+    r = _routes(c, 40, 6)
+    out, lse = qsa.paged_forward(d["q"], kp, vp, r.to(DEV), *where, SCALE)
+    _check(c, out, lse, routes=r)
+    k, v = _bf(_gen(26), 60, G, 256), _bf(_gen(27), 60, G, 256)
+    qsa.cache_append(k.to(DEV), v.to(DEV), kp, vp, *where)
+    for t in (0, 37, 59):
+        p = 90 + t
+        row = (int(table[0, p // page]), p % page)
+        assert torch.equal(kp[row].cpu(), k[t]) and torch.equal(vp[row].cpu(), v[t])
 
 
 @pytest.mark.parametrize("news", [1, 40])
@@ -232,6 +286,18 @@ def test_unseen_non_finite_rows_reach_nothing(news, value):
     r = torch.full((news, 8), -1, dtype=torch.int32)
     r[:, 0], r[:, 1] = 5, 299
     assert all(torch.isfinite(x).all() for x in _attend(c, routes=r))
+
+
+def test_a_non_finite_value_in_a_cut_item():
+    # V of the diagonal's keys, where the item's last tile lies in a range of its own
+    c = _cache([3000], [30], 64, 1, 28)
+    j = 2985                                             # seen by the last 15 tokens
+    c["vp"][int(c["table"][0, j // 64]), j % 64, 0, 5] = float("inf")
+    out, lse = _attend(c)
+    assert torch.isfinite(lse).all() and torch.isfinite(out[:15]).all()
+    assert (out[15:, :, 5] == float("inf")).all()
+    out[15:, :, 5] = 0
+    assert torch.isfinite(out).all()
 
 
 def test_large_scores_and_first_keys_that_dominate():
@@ -278,13 +344,15 @@ def test_cache_append(name, rot, interleaved):
         kw = dict(q=d["q"], inv_freq=f, interleaved=interleaved, mscale=m, out_q=out_q)
     got_q = qsa.cache_append(k.to(DEV), v.to(DEV), d["kp"], d["vp"], *where, **kw)
     at = [P.place(t, c["kv_len"].tolist(), c["cu_q"].tolist()) for t in range(T)]
-    pos = torch.tensor([0 if x is None else x[1] for x in at], dtype=torch.int32, device=DEV)
+    # (a length of -2^31 has positions that rope's int32 cannot name: their q rows are not compared)
+    named = torch.tensor([x is not None and x[1] >= -2**31 for x in at], device=DEV)
+    pos = torch.tensor([0 if x is None else max(x[1], -2**31) for x in at], dtype=torch.int32, device=DEV)
     k_ref = k
     if rot:  # the same rotation as rope's, bit for bit
         q_ref, k_ref = qsa.rope(d["q"], k.to(DEV), pos, f, interleaved=interleaved, mscale=m)
         k_ref = k_ref.cpu()
         of_none = torch.tensor([x is None for x in at], device=DEV)
-        assert (got_q[of_none] == 7.0).all() and torch.equal(got_q[~of_none], q_ref[~of_none])
+        assert (got_q[of_none] == 7.0).all() and torch.equal(got_q[named], q_ref[named])
     else:
         assert got_q is None
     kp, vp = P.append(_n(k_ref), _n(v), _n(c["kp"]), _n(c["vp"]), c["table"].numpy(), c["kv_len"].numpy(),

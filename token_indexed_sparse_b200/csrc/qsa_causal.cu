@@ -97,10 +97,10 @@ struct Seq {          // one sequence's new tokens (clamped to the packed rows)
 };
 __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
-  const int64_t z = min(max(static_cast<int64_t>(__ldg(a.c.cu_q + b + 1)), static_cast<int64_t>(0)), a.T);
+  const int64_t end = __ldg(a.c.cu_q + b + 1), z = min(max(end, static_cast<int64_t>(0)), a.T);
   s.start = static_cast<int>(min(max(static_cast<int64_t>(__ldg(a.c.cu_q + b)), static_cast<int64_t>(0)), z));
   s.n = static_cast<int>(z - s.start);
-  s.p0 = static_cast<int64_t>(__ldg(a.c.kv_len + b)) - s.n;
+  s.p0 = static_cast<int64_t>(__ldg(a.c.kv_len + b)) - (end - s.start);
   return s;
 }
 __device__ __forceinline__ int query_tiles(const Seq& s) {
@@ -178,7 +178,7 @@ struct Walk {
         if (++i == query_tiles(s)) {
           i = 0;
           do s = seq_of(a, ++b);
-          while (s.n == 0);
+          while (s.n == 0 && b + 1 < a.c.B);
         }
       }
     }

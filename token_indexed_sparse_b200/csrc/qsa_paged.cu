@@ -47,7 +47,7 @@ __device__ __forceinline__ float p_of(float s, float m) { return s == -INFINITY 
 // memory (linear probing) that holds slots and keeps the smallest slot of each ID, so which slot
 // stays does not depend on the threads' order; the slots that stayed are compacted in order.
 // Bound by instructions: few slots a thread and a table four times the row keep probes short.
-constexpr int kMaxRowThreads = 1024;
+constexpr int kMaxRowThreads = 1024, kMaxSlots = 16384;
 template <int PER>
 __global__ void __launch_bounds__(kMaxRowThreads)
 paged_rows_kernel(const int32_t* __restrict__ routes, CacheView cache, int n_sel, unsigned n_entries,
@@ -484,8 +484,9 @@ cudaError_t launch_paged_rows(const int32_t* routes, const CacheView& c, int64_t
   const int n_entries = n_sel < 16 ? 64 : (n_sel <= 8192 ? 4 * n_sel : 2 * n_sel);
   const int smem = 4 * (n_entries + n_sel), per = n_sel <= 2048 ? 2 : (n_sel <= 4096 ? 4 : 16);
   const auto kern = per == 2 ? paged_rows_kernel<2> : (per == 4 ? paged_rows_kernel<4> : paged_rows_kernel<16>);
-  if (smem > 47 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (per > 2) {  // the most that any row of this variant takes, whatever other threads launch meanwhile
+    const int most = per == 4 ? 4 * (4 * 4096 + 4096) : 4 * (2 * kMaxSlots + kMaxSlots);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   const int threads = ((n_sel + per - 1) / per + 31) / 32 * 32;
