@@ -147,3 +147,18 @@ def test_rope_frequencies():
                 dict(rotary_dim=64, factor=0.5), dict(rotary_dim=64, scaling="other")):
         with pytest.raises(ValueError):
             qsa.rope_frequencies(**{"device": "cpu", **bad})
+
+
+def test_the_short_way_leaves_what_it_does_not_take(lib):
+    # the compiled binding does nothing with what the Python one would convert or refuse
+    from token_indexed_sparse_b200 import qsa
+    short = qsa._short_way()
+    q, pos = torch.zeros(4, 12, 256, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    f = torch.ones(8, dtype=torch.float64)
+    for args in ((q, None, pos, f, False, 1.0, None, None, False), (q, q, pos), (1, 2, 3, 4, 5, 6, 7, 8, 9),
+                 (q, None, pos, f, False, "one", None, None, False)):
+        assert short.rope(*args) is NotImplemented
+    assert short.cache_append(*[q] * 12) is NotImplemented and short.paged_forward(*[q] * 11) is NotImplemented
+    assert short.paged_causal(*[q] * 12) is NotImplemented and short.paged_causal() is NotImplemented
+    with pytest.raises(TypeError):
+        short.bind(1, 2)

@@ -504,3 +504,80 @@ def test_refusals_on_the_device():
     with pytest.raises(qsa.QSAError) as e:
         qsa.paged_causal(d["q"], odd, odd, *where, SCALE)
     assert e.value.status == 2
+
+
+class _Declines:
+    """A compiled binding that takes nothing."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
+
+def test_the_short_and_the_long_way_agree(monkeypatch):
+    short = qsa._short_way()
+    taken = []
+
+    class Counts:
+        def __getattr__(self, name):
+            def call(*args):
+                r = getattr(short, name)(*args)
+                taken.append(r is not NotImplemented)
+                return r
+            return call
+
+    def everything():
+        c, s = _serving([200, 90, 31], [1, 40, 1], 60)
+        pos = torch.arange(s["q"].shape[0], dtype=torch.int32, device=DEV)
+        got = [*_step(s), s["kp"], s["vp"], *qsa.rope(s["q"], s["k"], pos, s["f"], interleaved=True, mscale=1.5),
+               *qsa.rope_backward(s["q"], None, pos, s["f"])[:1]]
+        where = (s["table"], s["kv_len"], s["cu_q"])
+        assert qsa.cache_append(s["k"], s["v"], s["kp"], s["vp"], *where) is None
+        out, lse = torch.empty_like(s["q"]), torch.empty(s["q"].shape[:2], device=DEV)
+        a, b = qsa.paged_causal(s["q"], s["kp"], s["vp"], *where, out=out, lse=lse)
+        assert a is out and b is lse
+        return got + [out, lse, s["kp"], s["vp"]]
+
+    monkeypatch.setattr(qsa, "_short", Counts())
+    a = everything()
+    assert len(taken) == 7 and all(taken)
+    monkeypatch.setattr(qsa, "_short", _Declines())
+    b = everything()
+    assert len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+    # what the short way leaves: routes in another layout, q in pieces
+    monkeypatch.setattr(qsa, "_short", Counts())
+    _, s = _serving([200, 90, 31], [1, 40, 1], 60)
+    where = (s["table"], s["kv_len"], s["cu_q"])
+    wide = torch.zeros(s["q"].shape[0], 24, 256, dtype=torch.bfloat16, device=DEV)
+    wide[:, 6:18] = s["q"]
+    r = s["routes"].t().contiguous().t()
+    x = qsa.paged_forward(wide[:, 6:18], s["kp"], s["vp"], r, *where)
+    y = qsa.paged_forward(s["q"], s["kp"], s["vp"], s["routes"], *where)
+    assert taken[-2:] == [False, True] and all(torch.equal(u, v) for u, v in zip(x, y))
+
+
+def test_refusals_are_the_same_both_ways(monkeypatch):
+    c = _cache([20], [2], 16, 1, 50)
+    d = {n: x.to(DEV) for n, x in c.items()}
+    where = (d["table"], d["kv_len"], d["cu_q"])
+    bad = [
+        lambda: qsa.paged_causal(d["q"], d["kp"], d["vp"], *where, -1.0),
+        lambda: qsa.paged_causal(d["q"], d["kp"], d["vp"], *where, sinks=-2),
+        lambda: qsa.paged_causal(d["q"], d["kp"], d["vp"], *where, workspace=d["q"]),
+        lambda: qsa.paged_causal(d["q"], d["kp"], d["vp"], *where, out=d["q"][:1]),
+        lambda: qsa.paged_forward(d["q"], d["kp"], d["vp"], d["table"].long(), *where),
+        lambda: qsa.paged_forward(d["q"], d["kp"].float(), d["vp"], d["table"], *where),
+        lambda: qsa.rope(d["q"], None, d["kv_len"], torch.ones(8, dtype=torch.float64, device=DEV)),
+        lambda: qsa.rope(d["q"], None, torch.zeros(2, dtype=torch.int32, device=DEV),
+                         torch.ones(9, dtype=torch.float64, device=DEV)),
+        lambda: qsa.cache_append(d["q"][:, :1], d["q"][:, :1], d["kp"], d["kp"], *where),
+        lambda: qsa.cache_append(d["q"][:, :2], d["q"][:, :2], d["kp"], d["vp"], *where),
+    ]
+
+    def said(call):
+        with pytest.raises(Exception) as e:
+            call()
+        return type(e.value), str(e.value)
+
+    both = [said(x) for x in bad]
+    monkeypatch.setattr(qsa, "_short", _Declines())
+    assert [said(x) for x in bad] == both

@@ -1,9 +1,11 @@
-"""Builds libqsa_b200.so (the CUDA kernels and the C ABI) in-tree with nvcc.
+"""Builds libqsa_b200.so (the CUDA kernels and the C ABI) in-tree with nvcc,
+and _qsa_torch.so (the short way from PyTorch tensors to it) with g++.
 
     python -m token_indexed_sparse_b200.build [--force]
 
 The library is compiled for sm_100a only and links the CUDA runtime statically,
-so it carries no dependency on the runtime bundled with PyTorch.
+so it carries no dependency on the runtime bundled with PyTorch; the binding is
+compiled against the PyTorch that imports it.
 """
 
 from __future__ import annotations
@@ -18,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqsa_b200.so")
+BINDING = os.path.join(PKG, "_qsa_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "qsa_torch.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["qsa_api.cu", "qsa_routes.cu", "qsa_forward.cu", "qsa_backward.cu", "qsa_noalloc.cu", "qsa_bitmap.cu", "qsa_selector.cu", "qsa_dkdv_union.cu", "qsa_cast.cu",
@@ -35,17 +39,44 @@ def _nvcc() -> str:
 
 def _inputs():
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "qsa.h")]
-    return deps
+    return [d for d in deps if d != BINDING_SOURCE]
+
+
+def _newer(out: str, inputs) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in inputs)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return _newer(LIB, _inputs())
+
+
+def build_binding(force: bool = False) -> str:
+    """Compiles _qsa_torch.so against the installed PyTorch."""
+    if not force and _newer(BINDING, [BINDING_SOURCE, os.path.join(INCLUDE, "qsa.h")]):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+                *cpp_extension.include_paths()]
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{i}" for i in includes], BINDING_SOURCE, "-o", tmp,
+           *[f"-L{p}" for p in cpp_extension.library_paths()], "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

@@ -1,5 +1,9 @@
 """Thin Python binding of libqsa_b200.so (argument marshalling only).
 
+The paged-cache calls, which a decode step makes every few microseconds, go
+through the compiled ``_qsa_torch`` where their arguments need nothing done to
+them, and through this file otherwise.
+
 Every step of the computation runs in the CUDA library; this module passes
 device pointers of PyTorch tensors and the current CUDA stream through the C ABI
 declared in ``include/qsa.h``.  There is no fallback: if the library is missing
@@ -17,6 +21,7 @@ import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqsa_b200.so")
 _lib = None
+_short = None  # _qsa_torch, bound to the library
 
 QSA_OK = 0
 
@@ -465,8 +470,24 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     return inv_freq.to(device), mscale
 
 
-# A decode step's calls take less time on the GPU than in here, so these helpers
-# read each property of a tensor once and raise from functions of their own.
+def _short_way():
+    """``_qsa_torch`` with the library's entry points (loads both once)."""
+    global _short
+    if _short is None:
+        lib = library()
+        try:
+            from . import _qsa_torch
+        except ImportError as e:
+            raise RuntimeError("_qsa_torch.so does not load; build it with "
+                               "`python -m token_indexed_sparse_b200.build`") from e
+        _qsa_torch.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.qsa_rope, lib.qsa_cache_append, lib.qsa_paged_forward, lib.qsa_paged_forward_workspace_size,
+            lib.qsa_paged_causal, lib.qsa_paged_causal_workspace_size)))
+        _short = _qsa_torch
+    return _short
+
+
+# The long way: the same calls for arguments that have to be converted first, or refused.
 
 def _enqueue(index: int, what: str, named, call, *args):
     """Runs a library call on CUDA device ``index`` (all tensors of ``named``,
@@ -552,13 +573,19 @@ def rope(q, k, positions, inv_freq, *, interleaved: bool = False, mscale: float 
     ``mscale`` as from ``rope_frequencies``; dims from rotary_dim up pass.  q and k
     may be slices of one projection (any strides between tokens and heads that
     are multiples of 8); ``out_q`` / ``out_k`` may be the inputs (in place)."""
-    return _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, 0)
+    r = (_short or _short_way()).rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, False)
+    if r is NotImplemented:
+        return _rope(q, k, positions, inv_freq, interleaved, mscale, out_q, out_k, 0)
+    return r if type(r) is tuple else _check(r, "qsa_rope")
 
 
 def rope_backward(grad_q, grad_k, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0,
                   out_q=None, out_k=None):
     """The gradient of ``rope``: ``(dq, dk)`` from the gradients of its outputs (the opposite turn)."""
-    return _rope(grad_q, grad_k, positions, inv_freq, interleaved, mscale, out_q, out_k, 1)
+    r = (_short or _short_way()).rope(grad_q, grad_k, positions, inv_freq, interleaved, mscale, out_q, out_k, True)
+    if r is NotImplemented:
+        return _rope(grad_q, grad_k, positions, inv_freq, interleaved, mscale, out_q, out_k, 1)
+    return r if type(r) is tuple else _check(r, "qsa_rope")
 
 
 def _bad_cache(k_pages, v_pages, block_table, kv_len, cu_q):
@@ -595,6 +622,10 @@ def cache_append(k_new, v_new, k_pages, v_pages, block_table, kv_len, cu_q, *, q
     With ``inv_freq`` (see ``rope_frequencies``) k is turned to its position in
     the cache first, and ``q`` [T, H, 256] with it: returns the turned q (into
     ``out_q``, which may be q itself), else None."""
+    r = (_short or _short_way()).cache_append(k_new, v_new, k_pages, v_pages, block_table, kv_len, cu_q, q, inv_freq,
+                                              interleaved, mscale, out_q)
+    if r is not NotImplemented:
+        return r if type(r) is not int else _check(r, "qsa_cache_append")
     k_rows = _rows(k_new, None, "k_new")
     T, G, _ = k_new.shape
     v_rows = _rows(v_new, T, "v_new")
@@ -655,6 +686,10 @@ def paged_forward(q, k_pages, v_pages, routes, block_table, kv_len, cu_q, scale:
     as in ``forward``).  Pools ``[n_pages, page_size, G, 256]``, ``block_table``
     [B, max_pages], ``kv_len`` [B] and ``cu_q`` [B + 1] int32.  Rows of no
     sequence are left as they were in ``out`` and ``lse``."""
+    r = (_short or _short_way()).paged_forward(q, k_pages, v_pages, routes, block_table, kv_len, cu_q, scale, out, lse,
+                                               workspace)
+    if r is not NotImplemented:
+        return r if type(r) is tuple else _check(r, "qsa_paged_forward")
     q, out, lse, T, H = _paged_io(q, out, lse)
     routes = _prep(routes, torch.int32, "routes")
     cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
@@ -677,6 +712,10 @@ def paged_causal(q, k_pages, v_pages, block_table, kv_len, cu_q, scale: float = 
     A token at position p sees the positions ``j <= p`` of its sequence, with
     ``window`` above 0 only those with ``j > p - window`` or ``j < sinks``.  The
     cache as in ``paged_forward``."""
+    r = (_short or _short_way()).paged_causal(q, k_pages, v_pages, block_table, kv_len, cu_q, scale, window, sinks, out,
+                                              lse, workspace)
+    if r is not NotImplemented:
+        return r if type(r) is tuple else _check(r, "qsa_paged_causal")
     q, out, lse, T, H = _paged_io(q, out, lse)
     cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
     ws = _workspace(paged_causal_workspace_size(T, H, cache[9], cache[6], cache[7], window, sinks), q.device,
