@@ -992,38 +992,56 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
   if (tid == 0 && *abort_flag) cont[blockIdx.x].status = 2;
 }
 
-// Joins the parts of the item that CTA range blockIdx.x begins and does not end.  An item of
-// many rows has few parts: a warp takes a row (row 16 y + warp of block y).  One with many parts (few
-// rows, a long cache): a block takes row y, y + 12, ..., its warps a sixteenth of the parts each,
-// added in order.  Also gathers the ranges' status into the call's.
-constexpr int kJoinWarps = 16, kJoinBlocks = kHeadsPerGroup, kBatch = 5;
-static_assert(kJoinWarps * kJoinBlocks >= kRows, "a warp per row");
+// Joins the parts of the items that were cut, in part order.  The blocks take units of work in turn:
+// 16 rows of an item with few parts (a warp a row), one row of an item with many (few rows, a
+// long cache: a sixteenth of the parts a warp).  Every block finds the units in the ranges' Conts (a grid
+// of a block per possible unit took 7 us to find that there is nothing to do).  Block 0 also gathers
+// the ranges' status into the call's.
+constexpr int kJoinWarps = 16, kBatch = 5;
 __global__ void __launch_bounds__(kJoinWarps * 32)
 causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ part_ml, const Cont* __restrict__ cont,
-                   int G, int* __restrict__ status, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+                   int n_ranges, int G, int* __restrict__ status, __nv_bfloat16* __restrict__ out,
+                   float* __restrict__ lse) {
   __shared__ float sO[kJoinWarps][kHeadDim];
   __shared__ float2 sMl[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x;
+  __shared__ int s_units[kMaxCtas + 1];  // units before range c's
+  __shared__ int s_warp[kJoinWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  static_assert(kMaxCtas <= kJoinWarps * 32, "a thread per range");
   after_previous();
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    int bad = 0;
-    for (int c = threadIdx.x; c < static_cast<int>(gridDim.x); c += blockDim.x) bad |= cont[c].status;
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *status = bad ? 2 : 0;
-  }
-  const Cont ct = cont[c0];
-  if (ct.rows == 0) return;
-  const int n = ct.c_last - c0 + 1;  // part 0: slot (c0, 1), part i: slot (c0 + i, 0)
-  auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
-  // this warp's sums (dims 8 lane on) of parts [a, z) of row r, against their largest maximum m
-  float o[8], l, m;
-  auto add = [&](int r, int a, int z) {
-    l = 0.f;
-    m = -INFINITY;
+  {
+    int mine = 0, bad = 0;
+    if (tid < n_ranges) {
+      const Cont ct = cont[tid];
+      bad = ct.status;
+      if (ct.rows > 0) mine = ct.c_last - tid + 1 <= kJoinWarps ? (ct.rows + kJoinWarps - 1) / kJoinWarps : ct.rows;
+    }
+    int up_to = mine;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0.f;
-    for (; a < z; a += kBatch) {  // a batch's reads in flight together
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up_to, o);
+      if (lane >= o) up_to += y;
+    }
+    if (lane == 31) s_warp[warp] = up_to;
+    bad = __syncthreads_or(bad);
+    for (int w = 0; w < warp; ++w) up_to += s_warp[w];
+    if (tid <= kMaxCtas) s_units[tid] = up_to - mine;
+    if (blockIdx.x == 0 && tid == 0) *status = bad ? 2 : 0;
+    __syncthreads();
+  }
+  for (int unit = blockIdx.x; unit < s_units[n_ranges]; unit += gridDim.x) {
+    int c0 = 0;
+    for (int o = 128; o > 0; o >>= 1)
+      if (c0 + o < n_ranges && s_units[c0 + o] <= unit) c0 += o;  // the last range with units at or before it
+    const Cont ct = cont[c0];
+    const int n = ct.c_last - c0 + 1;  // part 0: slot (c0, 1), part i: slot (c0 + i, 0)
+    auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
+    const bool few = n <= kJoinWarps;
+    const int r = few ? kJoinWarps * (unit - s_units[c0]) + warp : unit - s_units[c0];
+    // this warp's sums (dims 8 lane on) of parts [a, z) of row r, against their largest maximum m
+    float o[8] = {}, l = 0.f, m = -INFINITY;
+    const int z = r >= ct.rows ? 0 : (few ? n : n * (warp + 1) / kJoinWarps);
+    for (int a = few ? 0 : n * warp / kJoinWarps; a < z; a += kBatch) {  // a batch's reads in flight together
       float2 ml[kBatch];
       float4 u[kBatch], v[kBatch];
       float top = m;
@@ -1053,44 +1071,35 @@ causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ pa
         o[4] += v[i].x * f, o[5] += v[i].y * f, o[6] += v[i].z * f, o[7] += v[i].w * f;
       }
     }
-  };
-  auto row_of = [&](int r) {
     const int f = ct.first + r;
-    return (static_cast<int64_t>(ct.row0) + f / kHeadsPerGroup) * G * kHeadsPerGroup + ct.g * kHeadsPerGroup +
-           f % kHeadsPerGroup;
-  };
-  if (n <= kJoinWarps) {
-    const int r = kJoinWarps * blockIdx.y + warp;
-    if (r >= ct.rows) return;
-    add(r, 0, n);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t row = row_of(r);
-    *reinterpret_cast<uint4*>(out + row * kHeadDim + 8 * lane) =
-        make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
-                   pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
-    if (lane == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    return;
-  }
-  for (int r = blockIdx.y; r < ct.rows; r += kJoinBlocks) {
-    add(r, n * warp / kJoinWarps, n * (warp + 1) / kJoinWarps);
-    __syncthreads();
+    const int64_t row = (static_cast<int64_t>(ct.row0) + f / kHeadsPerGroup) * G * kHeadsPerGroup +
+                        ct.g * kHeadsPerGroup + f % kHeadsPerGroup;
+    if (few) {
+      if (r >= ct.rows) continue;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint4*>(out + row * kHeadDim + 8 * lane) =
+          make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                     pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+      if (lane == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      continue;
+    }
+    __syncthreads();  // (few is the block's)
 #pragma unroll
     for (int i = 0; i < 8; ++i) sO[warp][8 * lane + i] = o[i];
     if (lane == 0) sMl[warp] = make_float2(m, l);
     __syncthreads();
-    if (threadIdx.x >= kHeadDim) continue;
+    if (tid >= kHeadDim) continue;
     float top = -INFINITY, total = 0.f, y = 0.f;
 #pragma unroll
     for (int x = 0; x < kJoinWarps; ++x) top = fmaxf(top, sMl[x].x);
 #pragma unroll
     for (int x = 0; x < kJoinWarps; ++x) {
-      const float f = sMl[x].x == -INFINITY ? 1.f : exp2f(sMl[x].x - top);
-      total += sMl[x].y * f;
-      y += sO[x][threadIdx.x] * f;
+      const float g = sMl[x].x == -INFINITY ? 1.f : exp2f(sMl[x].x - top);
+      total += sMl[x].y * g;
+      y += sO[x][tid] * g;
     }
-    const int64_t row = row_of(r);
-    out[row * kHeadDim + threadIdx.x] = __float2bfloat16_rn(total == 0.f ? 0.f : y / total);
-    if (threadIdx.x == 0) lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    out[row * kHeadDim + tid] = __float2bfloat16_rn(total == 0.f ? 0.f : y / total);
+    if (tid == 0) lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
   }
 }
 
@@ -1138,9 +1147,9 @@ cudaError_t launch_paged_causal(const void* q, const void* k_pages, const void* 
                                               scale * kLog2e, part, ml, cont, static_cast<__nv_bfloat16*>(out), lse);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_after(causal_join_kernel, dim3(grid, kJoinBlocks), kJoinWarps * 32, 0, s,
-                      static_cast<const float*>(part), static_cast<const float2*>(ml), static_cast<const Cont*>(cont), G,
-                      status, static_cast<__nv_bfloat16*>(out), lse);
+  return launch_after(causal_join_kernel, dim3(2 * grid), kJoinWarps * 32, 0, s, static_cast<const float*>(part),
+                      static_cast<const float2*>(ml), static_cast<const Cont*>(cont), grid, G, status,
+                      static_cast<__nv_bfloat16*>(out), lse);
 }
 
 }  // namespace qsa
