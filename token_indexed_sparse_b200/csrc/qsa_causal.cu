@@ -91,30 +91,29 @@ struct Args {
 // items
 // ---------------------------------------------------------------------------
 
+// Positions are 32 bits here: a length is taken as -2^30 at least and the packed rows as 2^30 at
+// most, so what is below zero stays there and nothing wraps.
 struct Seq {          // one sequence's new tokens (clamped to the packed rows)
   int start, n;       // packed rows [start, start + n)
-  int64_t p0;         // position of the first
+  int p0;             // position of the first
 };
 __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
-  const int64_t end = __ldg(a.c.cu_q + b + 1), z = min(max(end, static_cast<int64_t>(0)), a.T);
-  s.start = static_cast<int>(min(max(static_cast<int64_t>(__ldg(a.c.cu_q + b)), static_cast<int64_t>(0)), z));
-  s.n = static_cast<int>(z - s.start);
-  s.p0 = static_cast<int64_t>(__ldg(a.c.kv_len + b)) - (end - s.start);
+  const int T = static_cast<int>(a.T), end = min(max(__ldg(a.c.cu_q + b + 1), 0), 1 << 30), z = min(end, T);
+  s.start = min(max(__ldg(a.c.cu_q + b), 0), z);
+  s.n = z - s.start;
+  s.p0 = max(__ldg(a.c.kv_len + b), -(1 << 30)) - (end - s.start);
   return s;
 }
 __device__ __forceinline__ int query_tiles(const Seq& s) {
   return (s.n * kHeadsPerGroup - 1) / kRows + (s.n > 0 ? 1 : 0);
 }
-__device__ __forceinline__ int64_t key_limit(const Args& a) {
-  return static_cast<int64_t>(a.c.max_pages) << a.c.page_shift;
-}
 // Keys [lo, hi) and [0, first) that a token at position p sees.
-__device__ __forceinline__ int row_hi(const Args& a, int64_t p) {
-  return static_cast<int>(max(static_cast<int64_t>(0), min(p + 1, key_limit(a))));
+__device__ __forceinline__ int row_hi(const Args& a, int p) {
+  return max(0, min(p + 1, a.c.max_pages << a.c.page_shift));
 }
-__device__ __forceinline__ int row_lo(const Args& a, int64_t p) {
-  return a.window > 0 ? static_cast<int>(max(static_cast<int64_t>(0), p + 1 - a.window)) : 0;
+__device__ __forceinline__ int row_lo(const Args& a, int p) {
+  return a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
 }
 __device__ __forceinline__ int first_keys(const Args& a) { return a.window > 0 ? a.sinks : 0; }
 
@@ -130,7 +129,7 @@ __device__ __forceinline__ Item item_of(const Args& a, const Seq& s, int i) {
   Item it;
   const int r0 = i * kRows;  // below n * 12 <= T * H, which fits 31 bits
   it.rows = min(kRows, s.n * kHeadsPerGroup - r0);
-  const int64_t pa = s.p0 + r0 / kHeadsPerGroup, pz = s.p0 + (r0 + it.rows - 1) / kHeadsPerGroup;
+  const int pa = s.p0 + r0 / kHeadsPerGroup, pz = s.p0 + (r0 + it.rows - 1) / kHeadsPerGroup;
   it.hi0 = row_hi(a, pa);
   it.hi1 = row_hi(a, pz);
   it.lo0 = row_lo(a, pa);
@@ -745,8 +744,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     Walk w(a, start, tiles);
     while (w.take(a)) {
       const bool live = 32 * wq < w.it.rows;
-      const int64_t r0 = static_cast<int64_t>(w.i) * kRows;
-      const int64_t p = w.s.p0 + (r0 + row) / kHeadsPerGroup;
+      const int r0 = w.i * kRows;
+      const int p = w.s.p0 + (r0 + row) / kHeadsPerGroup;
       const int hi = row < w.it.rows ? row_hi(a, p) : 0, lo = row < w.it.rows ? row_lo(a, p) : 0;
       const int n = w.x1 - w.x0;
       // Lane l's page of the l-th page of tile y, read a tile ahead of its use
@@ -974,8 +973,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       }
       if (tid == 0 && w.x0 == 0 && w.x1 < w.it.n) {  // the item goes on in the ranges behind this one
         Cont ct{};
-        ct.row0 = w.s.start + static_cast<int>(r0 / kHeadsPerGroup);
-        ct.first = static_cast<int>(r0 % kHeadsPerGroup);
+        ct.row0 = w.s.start + r0 / kHeadsPerGroup;
+        ct.first = r0 % kHeadsPerGroup;
         ct.rows = w.it.rows;
         ct.g = w.g;
         const int64_t item_end = t_end - (w.x1 - w.x0) + w.it.n;  // this piece is the range's last
