@@ -27,9 +27,12 @@
 //   warp 11     the next item's Q rows (cp.async into the 128-byte swizzle)
 // Tensor memory: O 256 columns, S / P two buffers of 128.
 //
-// Both products cost 1024 tensor cycles per tile (4096 multiply-adds a cycle and SM);
-// the exponentials take 1024 of the MUFU's, under them, so a long chunk is bound by the
-// tensor core and a decode step by the cache's bytes.
+// Both products cost 1024 tensor cycles per tile (4096 multiply-adds a cycle and SM), Q K^T
+// 1500 in fact: with M = N = 128 its operands come through shared memory in 94 cycles an
+// instruction, not 64.  A decode step is bound by the cache's bytes (48 sequences of up to
+// 32768 tokens: 0.27 ms, 6.3 TB/s), a long chunk by the time from S to P and back, about
+// 3200 cycles a tile, and by the power cap when kept up (2048 tokens behind 30000, 24 heads:
+// 1.23 ms, 1.3 PFLOP/s in a burst, 1.40 ms kept up; tensor pipe 64 % active, MUFU 32 %).
 //
 // Values that a row must not see: keys past the diagonal, outside the window, without a
 // page are masked in S.  P V multiplies every V row of the tile, and 0 * NaN is NaN, so in
