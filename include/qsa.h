@@ -452,9 +452,10 @@ qsa_status_t qsa_forward_noalloc(const void* q, const void* k, const void* v, co
  * them.
  *   q, q_out [T, H, 256], k, k_out [T, G, 256] BF16 with element strides between
  *   tokens and heads (multiples of 8; dims contiguous; 16-byte aligned).  G = 0:
- *   no k.  Any H >= 1, G >= 0.  An output is its own input (same pointer and
- *   strides: in place) or overlaps it nowhere, and its rows do not overlap (both
- *   checked); it overlaps nothing else that the call reads or writes.
+ *   no k.  H >= 1, G >= 0, H + G < 2^27 - 64, T * (H + G) <= 2^31 - 1.  An output
+ *   is its own input (same pointer and strides: in place) or overlaps it nowhere,
+ *   and its rows do not overlap (both checked); it overlaps nothing else that the
+ *   call reads or writes.
  *   positions [T] int32 (any value); inv_freq [rotary_dim / 2] double, finite;
  *   rotary_dim a multiple of 16, at most 256 (else QSA_ERR_UNSUPPORTED);
  *   0 < mscale < inf.
@@ -471,7 +472,7 @@ qsa_status_t qsa_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  * cache) k is rotated on the way, and q [T, H, 256], when given, to q_out (every
  * row that belongs to a sequence, with or without a page).  inv_freq NULL: k
  * as it is, and no q (QSA_ERR_INVALID_ARGUMENT with one).  Strides, in-place
- * rule and errors as in qsa_rope.
+ * rule and errors as in qsa_rope; H + 2 G < 2^27 - 64.
  */
 qsa_status_t qsa_cache_append(const void* k_new, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
                               int64_t v_token_stride, int64_t v_head_stride, const void* q, int64_t q_token_stride,

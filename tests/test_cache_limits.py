@@ -1,0 +1,46 @@
+"""Sizes at the limits of the paged-cache calls: refused on the host, before any
+CUDA work, where the kernels' 32-bit counts would not hold them.  Each call runs
+in a process of its own, so that one which ends the process fails its test only."""
+
+import subprocess
+import sys
+
+import pytest
+
+HEAD = """
+import ctypes
+from token_indexed_sparse_b200 import qsa
+lib, P = qsa.library(), ctypes.c_void_p
+
+def rope(T, H, G):
+    rows = [P(4096), 0, 256, P(1 << 50), 0, 256]
+    out = [P(4096), H * 256, 256, P(1 << 50), G * 256, 256]
+    return lib.qsa_rope(*rows, *out, P(256), P(256), T, H, G, 64, 0, 1.0, 0, None)
+
+def append(T, G, B=1, q=None):
+    rows = [P(4096), 0, 256, P(1 << 50), 0, 256, P(q), 0, 256, P(q), 0, 256]
+    return lib.qsa_cache_append(*rows, P(256) if q else None, 64, 0, 1.0, P(1 << 31), P(1 << 32), P(256), P(256),
+                                P(256), T, B, 4, 16, 3, 12 * G, G, None)
+"""
+
+
+@pytest.fixture(scope="module")
+def status():
+    from token_indexed_sparse_b200 import build
+    build.build()
+
+    def run(call):
+        r = subprocess.run([sys.executable, "-c", f"{HEAD}\nprint('status', {call})"], capture_output=True, text=True)
+        assert r.returncode == 0, f"the process ended with {r.returncode}: {r.stderr}"
+        return int(r.stdout.split("status")[1])
+
+    return run
+
+
+# 16 units a head, and 1024 behind them, have to fit 31 bits
+@pytest.mark.parametrize("call", ["rope(1, 2**28, 0)", "rope(1, 2**28 - 1, 1)", "rope(1, 2**27, 0)",
+                                  "rope(1, 2**27 - 64, 0)", "rope(1, 2**26, 2**26)", "rope(1, 2**31 - 1, 0)",
+                                  "append(1, 2**27)", "append(1, 2**31 // 14)", "append(1, 2**27 // 14)",
+                                  "append(1, 2**27 // 14, q=1 << 40)"])
+def test_heads_past_the_kernels_counts_are_refused(status, call):
+    assert status(call) == 1

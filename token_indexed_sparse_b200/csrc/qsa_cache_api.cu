@@ -15,6 +15,9 @@ namespace {
 constexpr int kMaxSel = 16384;
 constexpr int kMinPage = 16;
 constexpr int64_t kMaxLen = int64_t{1} << 30;  // positions that a block table can name
+// Heads of a token that the rotation and the append take: their kernels count its 16 units a head, and
+// up to 1024 behind them, in 32 bits.
+constexpr int64_t kMaxRotaryHeads = (INT32_MAX - 1024) / 16;
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -126,7 +129,8 @@ qsa_status_t qsa_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
                       const int32_t* positions, const double* inv_freq, int64_t T, int H, int G, int rotary_dim,
                       int interleaved, float mscale, int backward, qsa_stream_t stream) {
   if (!positions || T < 1 || T > (int64_t{1} << 30) || H < 1 || G < 0) return QSA_ERR_INVALID_ARGUMENT;
-  if (T > INT32_MAX / (static_cast<int64_t>(H) + G)) return QSA_ERR_INVALID_ARGUMENT;
+  const int64_t heads = static_cast<int64_t>(H) + G;
+  if (T > INT32_MAX / heads || heads > kMaxRotaryHeads) return QSA_ERR_INVALID_ARGUMENT;
   QSA_CHECK(check_rotary(inv_freq, rotary_dim, mscale));
   QSA_CHECK(check_rows(q, q_token_stride, q_head_stride, T, H));
   QSA_CHECK(check_out_rows(q_out, q_out_token_stride, q_out_head_stride, q, q_token_stride, q_head_stride, T, H));
@@ -151,6 +155,7 @@ qsa_status_t qsa_cache_append(const void* k_new, int64_t k_token_stride, int64_t
                               int page_size, int64_t max_pages, int H, int G, qsa_stream_t stream) {
   if (!k_pages || !v_pages || k_pages == v_pages || !block_table || !kv_len || !cu_q) return QSA_ERR_INVALID_ARGUMENT;
   QSA_CHECK(check_heads(T, H, G));
+  if (H + 2 * static_cast<int64_t>(G) > kMaxRotaryHeads) return QSA_ERR_INVALID_ARGUMENT;
   QSA_CHECK(check_cache(B, n_pages, page_size, max_pages));
   if (inv_freq) QSA_CHECK(check_rotary(inv_freq, rotary_dim, mscale));
   QSA_CHECK(check_rows(k_new, k_token_stride, k_head_stride, T, G));

@@ -94,7 +94,8 @@ __device__ __forceinline__ void fill_turns(float2 (*cs)[kUnits * kCsUnit], const
   }
 }
 
-// A block's units, four per thread and round: unit u is unit j of head h of token tok.
+// A block's units, `ahead` per thread and round: unit u is unit j of head h of token tok.  They are counted in
+// 32 bits: a block has 1024 at most or one token's heads, which the entry points bound.
 struct Unit {
   int tok, h, j;
 };
