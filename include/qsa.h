@@ -435,8 +435,8 @@ qsa_status_t qsa_forward_noalloc(const void* q, const void* k, const void* v, co
  * Several streams may read one cache at once; a call that writes it has to be
  * ordered against the others by the caller.
  *   page_size: a power of two, 16 or more (else QSA_ERR_UNSUPPORTED); n_pages *
- *   page_size at most 2^31 - 1; max_pages * page_size at most 2^30; B >= 1;
- *   1 <= T <= 2^30; T * H <= 2^31 - 1; H = 12 G.
+ *   page_size at most 2^31 - 1; max_pages * page_size at most 2^30; 1 <= B
+ *   <= 2^30; 1 <= T <= 2^30; T * H <= 2^31 - 1; H = 12 G.
  * Other conventions (alignment, workspace, stream, errors) as at the top.
  */
 

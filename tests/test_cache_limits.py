@@ -44,3 +44,14 @@ def status():
                                   "append(1, 2**27 // 14, q=1 << 40)"])
 def test_heads_past_the_kernels_counts_are_refused(status, call):
     assert status(call) == 1
+
+
+CAUSAL = "lib.qsa_paged_causal(*[P(256)] * 6, 8, {B}, 4, 16, 3, 12, 1, 0, 0, 1.0, *[P(256)] * 3, 1 << 40, None)"
+ROUTED = "lib.qsa_paged_forward(*[P(256)] * 7, 8, {B}, 4, 16, 3, 12, 1, 4, 1.0, *[P(256)] * 3, 1 << 40, None)"
+
+
+# the search for a row's sequence looks up to 31 offsets past B, the plan up to 383
+@pytest.mark.parametrize("B", ["2**31 - 1", "2**31 - 384", "2**30 + 1"])
+@pytest.mark.parametrize("call", ["append(8, 1, {B})", CAUSAL, ROUTED])
+def test_more_sequences_than_the_searches_count_are_refused(status, call, B):
+    assert status(call.format(B=B)) == 1

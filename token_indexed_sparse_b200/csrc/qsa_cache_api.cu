@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kMaxSel = 16384;
 constexpr int kMinPage = 16;
+constexpr int kMaxSeqs = 1 << 30;                // the searches over B step past it in 32 bits
 constexpr int64_t kMaxLen = int64_t{1} << 30;  // positions that a block table can name
 // Heads of a token that the rotation and the append take: their kernels count its 16 units a head, and
 // up to 1024 behind them, in 32 bits.
@@ -37,7 +38,7 @@ qsa_status_t check_heads(int64_t T, int H, int G) {
 }
 
 qsa_status_t check_cache(int B, int64_t n_pages, int page_size, int64_t max_pages) {
-  if (B < 1 || n_pages < 1 || page_size < 1 || max_pages < 1) return QSA_ERR_INVALID_ARGUMENT;
+  if (B < 1 || B > kMaxSeqs || n_pages < 1 || page_size < 1 || max_pages < 1) return QSA_ERR_INVALID_ARGUMENT;
   if (page_size < kMinPage || (page_size & (page_size - 1)) != 0) return QSA_ERR_UNSUPPORTED;
   if (n_pages > INT32_MAX / page_size || max_pages > kMaxLen / page_size) return QSA_ERR_INVALID_ARGUMENT;
   return QSA_OK;
