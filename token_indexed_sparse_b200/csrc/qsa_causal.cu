@@ -464,11 +464,11 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     t_end = n_tiles * (c + 1) / n_ctas;
     auto locate = [&](int seq, int i, long long w, long long at) {  // if the range begins in this query tile
       if (t_begin < at || t_begin >= at + w) return;
-      const int n = static_cast<int>(w / a.G), off = static_cast<int>(t_begin - at);
+      const long long n = w / a.G, off = t_begin - at;  // key tiles of all groups may pass 31 bits
       start[0] = seq;
       start[1] = i;
-      start[2] = off / n;
-      start[3] = off % n;
+      start[2] = static_cast<int>(off / n);
+      start[3] = static_cast<int>(off - off / n * n);
     };
     if (batches == 1) {  // what the scan above has in hand
       locate(seq0, tile0, w0, incl0 - w0);
