@@ -1002,9 +1002,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
 // the ranges' status into the call's.
 constexpr int kJoinWarps = 16, kBatch = 5;
 __global__ void __launch_bounds__(kJoinWarps * 32)
-causal_join_kernel(const float* __restrict__ part, const float2* __restrict__ part_ml, const Cont* __restrict__ cont,
-                   int n_ranges, int G, int* __restrict__ status, __nv_bfloat16* __restrict__ out,
-                   float* __restrict__ lse) {
+causal_join_kernel(const float* part, const float2* part_ml, const Cont* cont, int n_ranges, int G,
+                   int* __restrict__ status, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   __shared__ float sO[kJoinWarps][kHeadDim];
   __shared__ float2 sMl[kJoinWarps];
   __shared__ int s_units[kMaxCtas + 1];  // units before range c's

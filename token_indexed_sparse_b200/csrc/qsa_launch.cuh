@@ -6,6 +6,10 @@
 // kernel wrote, it has to wait in after_previous, which returns once the kernel before it has ended and
 // its writes can be seen.  That kernel must itself be ordered behind what came before it
 // (launched without this, or past its own after_previous), so the order is whole.
+//
+// What an earlier kernel of the chain writes is not read-only while such a kernel lives, even past the
+// wait: it is read by plain loads, through pointers that are not `const __restrict__`, never by __ldg
+// (ld.global.nc), which the compiler may move across the wait.
 #pragma once
 
 #include <cuda_runtime.h>

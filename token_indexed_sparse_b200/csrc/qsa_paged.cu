@@ -124,9 +124,9 @@ paged_rows_kernel(const int32_t* __restrict__ routes, CacheView cache, int n_sel
 
 __global__ void __launch_bounds__(kThreads, kCps)
 paged_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
-             const __nv_bfloat16* __restrict__ v, const int32_t* __restrict__ row_cnt,
-             const int32_t* __restrict__ row_cols, int n_sel, unsigned n_items, int G, int splits, float scale_log2,
-             float* __restrict__ partial, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+             const __nv_bfloat16* __restrict__ v, const int32_t* row_cnt, const int32_t* row_cols,
+             int n_sel, unsigned n_items, int G, int splits, float scale_log2, float* partial,
+             __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -161,14 +161,14 @@ paged_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restric
     key_end = min(static_cast<int>(n * (part + 1) / splits) * kKeys, cnt);
     first = true;
     const unsigned nx = it + gridDim.x;
-    cnt_next = nx < n_items ? __ldg(row_cnt + row_of_item(nx)) : 0;
+    cnt_next = nx < n_items ? row_cnt[row_of_item(nx)] : 0;
   };
   // Lane j (and j + 8, ...) holds the pool row of the warp's key j of the chunk, -1 behind the last.
   auto rows_of = [&]() {
     const int i = key0 + 8 * warp + (lane & 7);
-    return it < n_items && i < key_end ? __ldg(row_cols + static_cast<int64_t>(t) * n_sel + i) : -1;
+    return it < n_items && i < key_end ? row_cols[static_cast<int64_t>(t) * n_sel + i] : -1;
   };
-  enter(it < n_items ? __ldg(row_cnt + row_of_item(it)) : 0);
+  enter(it < n_items ? row_cnt[row_of_item(it)] : 0);
   int row = rows_of();
   // Issues the chunk into `stage`, records its descriptor, advances.
   auto issue = [&](int stage) {
@@ -395,7 +395,7 @@ paged_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restric
 constexpr int kManyParts = 8;
 template <bool MANY>
 __global__ void __launch_bounds__(MANY ? 256 : kHeadsPerGroup * 32)
-paged_join_kernel(const float* __restrict__ partial, const int32_t* __restrict__ row_cnt, int G, int splits,
+paged_join_kernel(const float* partial, const int32_t* row_cnt, int G, int splits,
                   __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   __shared__ float sO[MANY ? 8 : 1][kHeadDim];
   __shared__ float sL[8];
@@ -405,7 +405,7 @@ paged_join_kernel(const float* __restrict__ partial, const int32_t* __restrict__
   const float* base = partial + static_cast<int64_t>(item) * splits * kPartFloats;
   const float* ml = base + kHeadsPerGroup * kPartRow + 2 * h;
   after_previous();
-  const bool none = __ldg(row_cnt + item / G) < 0;
+  const bool none = row_cnt[item / G] < 0;
   float m = -INFINITY;
   for (int i = lane; i < splits; i += 32) m = fmaxf(m, ml[static_cast<int64_t>(i) * kPartFloats]);
   if (none) return;  // a row of no sequence (uniform)
