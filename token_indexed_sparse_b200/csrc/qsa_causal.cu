@@ -95,18 +95,19 @@ struct Args {
 // items
 // ---------------------------------------------------------------------------
 
-// Positions are 32 bits here: a length is taken as -2^30 at least and the packed rows as 2^30 at
-// most, so what is below zero stays there and nothing wraps.
+// Positions are 32 bits here: a first position is taken as -2^30 at least and the packed rows are below 2^28,
+// so what is below zero stays there and nothing wraps.
 struct Seq {          // one sequence's new tokens (clamped to the packed rows)
   int start, n;       // packed rows [start, start + n)
   int p0;             // position of the first
 };
 __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
-  const int T = static_cast<int>(a.T), end = min(max(__ldg(a.c.cu_q + b + 1), 0), 1 << 30), z = min(end, T);
+  const int end = __ldg(a.c.cu_q + b + 1), z = min(max(end, 0), static_cast<int>(a.T));
   s.start = min(max(__ldg(a.c.cu_q + b), 0), z);
   s.n = z - s.start;
-  s.p0 = max(__ldg(a.c.kv_len + b), -(1 << 30)) - (end - s.start);
+  const int64_t p0 = static_cast<int64_t>(__ldg(a.c.kv_len + b)) - (static_cast<int64_t>(end) - s.start);
+  s.p0 = static_cast<int>(max(p0, static_cast<int64_t>(-(1 << 30))));
   return s;
 }
 __device__ __forceinline__ int query_tiles(const Seq& s) {
