@@ -6,6 +6,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 HEAD = """
 import ctypes
@@ -55,3 +56,25 @@ ROUTED = "lib.qsa_paged_forward(*[P(256)] * 7, 8, {B}, 4, 16, 3, 12, 1, 4, 1.0, 
 @pytest.mark.parametrize("call", ["append(8, 1, {B})", CAUSAL, ROUTED])
 def test_more_sequences_than_the_searches_count_are_refused(status, call, B):
     assert status(call.format(B=B)) == 1
+
+
+@pytest.mark.parametrize("name", ["window", "sinks"])
+@pytest.mark.parametrize("value", [2**31, 2**32, 2**32 + 5, -2**31 - 1])
+def test_the_binding_refuses_what_32_bits_do_not_hold(status, name, value):
+    from token_indexed_sparse_b200 import qsa
+    x, i = torch.zeros(2, 12, 256, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    pages = torch.zeros(1, 16, 1, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
+        qsa.paged_causal(x, pages, pages, i[None], i[:1], i, **{name: value})
+    with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
+        qsa.paged_causal_workspace_size(2, 12, 1, 16, 1, **{name: value})
+
+
+def test_the_workspace_sizes_refuse_what_32_bits_do_not_hold(status):
+    from token_indexed_sparse_b200 import qsa
+    for bad in ((2**32 + 12, 1, 4, 16), (12, 2**32 + 1, 4, 16), (12, 1, 2**32 + 4, 16), (12, 1, 4, 2**32 + 16)):
+        with pytest.raises(ValueError, match="32 bits"):
+            qsa.paged_forward_workspace_size(2, *bad, 3)
+    x = torch.zeros(1, 1, 256, dtype=torch.bfloat16).expand(1, 2**32 + 12, 256)
+    with pytest.raises(ValueError, match="heads of q must fit 32 bits"):
+        qsa.rope(x, None, torch.zeros(1, dtype=torch.int32), torch.ones(8, dtype=torch.float64))

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 
 import torch
@@ -506,6 +507,14 @@ def _enqueue(index: int, what: str, named, call, *args):
         raise QSAError(st, what)
 
 
+def _int32(x, name: str) -> int:
+    """An int argument of the library (ctypes would keep the low 32 bits of a larger one)."""
+    x = operator.index(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _bad_rows(x: torch.Tensor, T: int | None, name: str):
     if x.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
@@ -520,6 +529,7 @@ def _rows(x: torch.Tensor, T: int | None, name: str):
     if (x.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != 256 or stride[2] != 1
             or (T is not None and shape[0] != T)):
         _bad_rows(x, T, name)
+    _int32(shape[1], f"heads of {name}")
     # the stride of an axis of length one is free
     return x.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
@@ -609,7 +619,10 @@ def _cache(k_pages, v_pages, block_table, kv_len, cu_q, T: int, H: int):
             or v_pages.shape != shape or not k_pages.is_contiguous() or not v_pages.is_contiguous()
             or block_table.dtype != torch.int32 or len(table) != 2 or not block_table.is_contiguous()):
         _bad_cache(k_pages, v_pages, block_table, kv_len, cu_q)
-    B = table[0]
+    B = _int32(table[0], "rows of block_table")
+    _int32(shape[1], "the page size")
+    _int32(shape[2], "KV heads")
+    _int32(H, "query heads")
     return (block_table.data_ptr(), _vector(kv_len, B, torch.int32, "kv_len"),
             _vector(cu_q, B + 1, torch.int32, "cu_q (one longer than kv_len)"),
             T, B, shape[0], shape[1], table[1], H, shape[2])
@@ -670,11 +683,15 @@ def _paged_io(q, out, lse):
 
 @functools.lru_cache(maxsize=1024)
 def paged_forward_workspace_size(T, H, G, n_sel, page_size, max_pages) -> int:
+    for x, name in ((H, "H"), (G, "G"), (n_sel, "n_sel"), (page_size, "page_size")):
+        _int32(x, name)
     return int(library().qsa_paged_forward_workspace_size(T, H, G, n_sel, page_size, max_pages))
 
 
 @functools.lru_cache(maxsize=1024)
 def paged_causal_workspace_size(T, H, G, page_size, max_pages, window: int = 0, sinks: int = 0) -> int:
+    for x, name in ((H, "H"), (G, "G"), (page_size, "page_size"), (window, "window"), (sinks, "sinks")):
+        _int32(x, name)
     return int(library().qsa_paged_causal_workspace_size(T, H, G, page_size, max_pages, window, sinks))
 
 
@@ -695,7 +712,7 @@ def paged_forward(q, k_pages, v_pages, routes, block_table, kv_len, cu_q, scale:
     cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
     if routes.dim() != 2 or routes.shape[0] != T:
         raise ValueError("routes must have one row per query")
-    n_sel = routes.shape[1]
+    n_sel = _int32(routes.shape[1], "the length of a row of routes")
     ws = _workspace(paged_forward_workspace_size(T, H, cache[9], n_sel, cache[6], cache[7]), q.device, workspace)
     _enqueue(q.get_device(), "qsa_paged_forward",
              (("k_pages", k_pages), ("v_pages", v_pages), ("routes", routes), ("block_table", block_table),
@@ -716,6 +733,7 @@ def paged_causal(q, k_pages, v_pages, block_table, kv_len, cu_q, scale: float = 
                                               lse, workspace)
     if r is not NotImplemented:
         return r if type(r) is tuple else _check(r, "qsa_paged_causal")
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
     q, out, lse, T, H = _paged_io(q, out, lse)
     cache = _cache(k_pages, v_pages, block_table, kv_len, cu_q, T, H)
     ws = _workspace(paged_causal_workspace_size(T, H, cache[9], cache[6], cache[7], window, sinks), q.device,
