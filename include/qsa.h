@@ -487,9 +487,9 @@ qsa_status_t qsa_cache_append(const void* k_new, int64_t k_token_stride, int64_t
  * sequence (a set, as there; an ID is valid iff 0 <= r < kv_len and the position
  * has a row; no causal mask is added).  q, out [T, H, 256] BF16 and lse [T, H]
  * float32 as in qsa_forward; a row with no valid route gives zero output and -inf
- * LSE.  K/V rows that a token does not see are never read for it.  Few rows with
- * long lists are split over the SMs and joined in a fixed order: results are bit
- * for bit the same from run to run.
+ * LSE, and so does one whose scores are all -inf.  K/V rows that a token does not
+ * see are never read for it.  Few rows with long lists are split over the SMs and
+ * joined in a fixed order: results are bit for bit the same from run to run.
  */
 size_t qsa_paged_forward_workspace_size(int64_t T, int H, int G, int n_sel, int page_size, int64_t max_pages);
 qsa_status_t qsa_paged_forward(const void* q, const void* k_pages, const void* v_pages, const int32_t* routes,

@@ -370,7 +370,7 @@ paged_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restric
           if (second) ml[gq + 8] = make_float2(m1, t1);
         }
       } else {
-        const float i0 = 1.f / t0, i1 = 1.f / t1;
+        const float i0 = t0 == 0.f ? 0.f : 1.f / t0, i1 = t1 == 0.f ? 0.f : 1.f / t1;  // 0: all scores -inf
         __nv_bfloat16* orow = out + qrow0 * kHeadDim;
 #pragma unroll
         for (int nt = 0; nt < kNt; ++nt) {
