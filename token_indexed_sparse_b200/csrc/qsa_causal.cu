@@ -68,7 +68,8 @@ constexpr int kOffTmem = kOffBar + kBars * 8;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kOffPoison = kOffAbort + 4;      // [3]: the item saw non-finite V it had to take out
 constexpr int kOffStart = kOffPoison + 12;     // the CTA's first tile: sequence, query tile, group, tile
-constexpr int kSmem = kOffStart + 16;          // no room to align the base: checked instead
+constexpr int kOffTile = kOffStart + 16;       // tiles whose scores have been issued
+constexpr int kSmem = kOffTile + 4;            // no room to align the base: checked instead
 static_assert(kSmem <= 232448, "shared memory per block");
 constexpr uint32_t kSpin = 1u << 22;           // polls before a wait gives up (seconds)
 constexpr uint32_t kColS = 256;                // tensor-memory columns: O [0, 256), S0, S1
@@ -370,14 +371,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
-// Bounded wait that also gives up once another role has.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+// Polls a barrier kSpin times at most, and no longer once a role has given up.
+__device__ __forceinline__ bool poll_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   bool ok = mbar_try(bar, parity);
 #pragma unroll 1
   for (uint32_t it = 0; !ok && it < kSpin; ++it) {
     ok = mbar_try(bar, parity);
     if ((it & 255) == 255 && *abort_flag) break;
   }
+  return ok;
+}
+// Bounded wait that also gives up once another role has.  For what takes a few tiles' time.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = poll_bar(bar, parity, abort_flag);
   if (!ok) *abort_flag = 1;
   return ok;
 }
@@ -389,6 +395,20 @@ __device__ __forceinline__ void converge() {
 // The same for a whole warp: every lane polls (and so has the barrier's ordering itself), all agree.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+}
+
+// A whole warp's wait for the end of an item, which may have millions of key tiles: its polls start over as
+// long as tiles are issued (whoever issues them waits a tile's time at most, and gives up by itself).
+__device__ __forceinline__ bool warp_wait_item(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               volatile int* tile) {
+  for (;;) {
+    const int seen = __shfl_sync(0xffffffffu, *tile, 0);
+    if (__all_sync(0xffffffffu, poll_bar(bar, parity, abort_flag))) return true;
+    const bool stuck = *abort_flag || *tile == seen;
+    if (__shfl_sync(0xffffffffu, stuck, 0)) break;
+  }
+  *abort_flag = 1;
+  return false;
 }
 
 struct Ring {  // position in the ring of units
@@ -429,6 +449,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
   const int H = a.G * kHeadsPerGroup;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffAbort);
   int* start = reinterpret_cast<int*>(smem + kOffStart);
+  volatile int* tile = reinterpret_cast<volatile int*>(smem + kOffTile);
   auto bar = [&](int i) { return sb + kOffBar + 8 * i; };
 
   if (tid == 0) {
@@ -499,6 +520,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     mbar_init(bar(kBDrain), 1);
     mbar_init(bar(kBDrain + 1), 1);
     *abort_flag = 0;
+    *tile = 0;
     for (int i = 0; i < 3; ++i) reinterpret_cast<int*>(smem + kOffPoison)[i] = 0;
     mbar_fence_init();
   }
@@ -625,6 +647,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             if (ok && y < 2) ok = landed();
             if (!ok) break;
             fence_after();
+            *tile = static_cast<int>(tau + 1);
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
               const uint64_t kd = k_desc + ring.slot * (kUnitBytes >> 4), qd = q_desc + u * (2 * kRows * 128 >> 4);
@@ -695,7 +718,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     Walk w(a, start, tiles);
     bool ok = true;
     while (w.take(a)) {
-      if (w.k > 0) ok = warp_wait(bar(kBQEmpty), (w.k - 1) & 1, abort_flag);
+      if (w.k > 0) ok = warp_wait_item(bar(kBQEmpty), (w.k - 1) & 1, abort_flag, tile);
       if (!ok) break;
       // a 512-byte row an instruction; rows past the last are zeros, whose products draw less power than
       // leftovers (a decode step of 12 rows kept up for a second: 315 us against 327)
