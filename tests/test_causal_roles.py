@@ -214,7 +214,7 @@ class Model:
                 break
             self.pipe["S"].append(("arrival", self.q_empty.arrive))
             yield
-        if not ok:
+        if not ok or self.variant != "only who gave up drains":
             yield from self.finish("S")
 
     def sums_of(self, t, k, y, u):
@@ -252,7 +252,7 @@ class Model:
                 yield
             if not ok:
                 break
-        if not ok:
+        if not ok or self.variant != "only who gave up drains":
             yield from self.finish("O")
 
     # ---- softmax
@@ -357,6 +357,13 @@ def test_a_long_item_is_not_given_up():
         assert not Model([(60, 4), (2, 1), (30, 2)], rng).run().abort
 
 
+@pytest.mark.parametrize("quits", ["producer", "loader", "S", "O", "softmax"])
+@pytest.mark.parametrize("seed", range(30))
+def test_every_role_ends_when_one_gives_up(quits, seed):
+    rng = random.Random(5000 + seed)
+    Model(_pieces(rng), rng, quits=quits).run()
+
+
 @pytest.mark.parametrize("variant", ["one budget for an item", "V by parity alone", "the other unit",
                                      "no meeting at an item's end"])
 def test_a_wait_changed_is_caught(variant):
@@ -364,6 +371,17 @@ def test_a_wait_changed_is_caught(variant):
         rng = random.Random(1000 + seed)
         try:
             Model(_pieces(rng) + [(12, 4), (1, 1)], rng, variant).run()
+        except Bad:
+            return
+    raise AssertionError(f"no schedule showed the mistake: {variant}")
+
+
+@pytest.mark.parametrize("variant", ["copies left in flight", "only who gave up drains"])
+def test_a_way_out_that_leaves_work_behind_is_caught(variant):
+    for seed in range(400):
+        rng = random.Random(1000 + seed)
+        try:
+            Model(_pieces(rng), rng, variant, quits=rng.choice(["producer", "loader", "S", "O", "softmax"])).run()
         except Bad:
             return
     raise AssertionError(f"no schedule showed the mistake: {variant}")

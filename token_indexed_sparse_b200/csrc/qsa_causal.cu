@@ -706,11 +706,10 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
           }
         }
       }
-      if (!ok) {  // the products in flight end before tensor memory is freed (bounded)
-        const int i = kBDrain + (warp == kMmaO ? 1 : 0);
-        commit(bar(i));
-        mbar_wait(bar(i), 0);
-      }
+      // The products in flight end before tensor memory is freed, whoever has given up meanwhile (bounded).
+      const int i = kBDrain + (warp == kMmaO ? 1 : 0);
+      commit(bar(i));
+      mbar_wait(bar(i), 0);
     }
     __syncwarp();
   } else if (warp >= kLoader) {
@@ -747,8 +746,8 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     // ------------------------------------------------------------ softmax
     // Thread (half, row): keys 64 half .. 64 half + 63 of every tile.  Both halves of a tile at once
     // (against a tile per warpgroup, two at a time) halve the time between S and P, which is
-    // what keeps the tensor core waiting.  A wait that gives up does not end the walk: every wait
-    // after it returns at once, so the hardware barriers below always meet.
+    // what keeps the tensor core waiting.  A wait that gives up does not end the walk: no wait after it
+    // polls, so the hardware barriers below always meet.
     const int half = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     volatile float* sX = reinterpret_cast<volatile float*>(smem + kOffX);
@@ -758,8 +757,9 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     const int first = first_keys(a);
     uint32_t tau = 0, units = 0;  // tiles so far, ring units before the piece
     uint32_t ex = 0;              // exchanges so far
+    bool given_up = false;
     auto wait = [&](int i, uint32_t parity) {
-      wait_bar(bar(i), parity, abort_flag);
+      if (!given_up) given_up = !wait_bar(bar(i), parity, abort_flag);
       converge();
     };
     // the other thread's value of the row (two buffers in turn: a buffer is written again only after
