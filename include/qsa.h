@@ -444,12 +444,12 @@ qsa_status_t qsa_forward_noalloc(const void* q, const void* k, const void* v, co
  * Rotary positions.  Pair i < rotary_dim / 2 of every head turns by the angle
  * positions[t] * inv_freq[i] and grows by mscale:
  *   y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x1 sin a + x2 cos a),
- * computed in FP32 from angles kept to 2^-32 of a turn, rounded once.  Pair i is
- * dims (2i, 2i + 1) when `interleaved`, else (i, i + rotary_dim / 2); dims from
- * rotary_dim up pass unchanged.  With `backward` nonzero the turn is by -a: the
- * gradient with respect to x from the gradient with respect to y.  Scaled
- * positions (long contexts) come as the frequencies and the mscale that go with
- * them.
+ * computed in FP32, rounded once; a is right to 2^-25 of a turn at any position,
+ * for |inv_freq| up to 2^40.  Pair i is dims (2i, 2i + 1) when `interleaved`, else
+ * (i, i + rotary_dim / 2); dims from rotary_dim up pass unchanged.  With `backward`
+ * nonzero the turn is by -a: the gradient with respect to x from the gradient with
+ * respect to y.  Scaled positions (long contexts) come as the frequencies and the
+ * mscale that go with them.
  *   q, q_out [T, H, 256], k, k_out [T, G, 256] BF16 with element strides between
  *   tokens and heads (multiples of 8; dims contiguous; 16-byte aligned).  G = 0:
  *   no k.  H >= 1, G >= 0, H + G < 2^27 - 64, T * (H + G) <= 2^31 - 1.  An output

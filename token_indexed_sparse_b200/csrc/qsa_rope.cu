@@ -8,10 +8,12 @@
 // the gradient is m times the opposite rotation: the same kernel with -sin.
 //
 // Angles: pos * f_i reaches 1e6 radians, where 32 bits keep 0.06 of a radian.
-// The turn count f_i / (2 pi) mod 1 is taken once in 64-bit floating point as a
-// fraction of 2^64; times the integer position, modulo 2^64, it is the angle's
-// fraction of a turn with no range reduction, and its top 32 bits as half-turns
-// go to sincospi (error about 1e-7 of a radian).
+// The turn count f_i / (2 pi) mod 1 is taken in two 64-bit floating-point parts (one
+// alone leaves 2^-25 of a turn at position 2^31 for f = 1, and more for faster pairs)
+// as a fraction of 2^64, right to a unit; times the integer position, modulo 2^64, it
+// is the angle's fraction of a turn with no range reduction, right to 2^-33.  Its top
+// 32 bits as half-turns, rounded to FP32, go to sincospi: 2^-26 of a turn, 1e-7 of a
+// radian, is what that leaves.
 //
 // Bound by memory: every 16-byte piece is read and written once, past the caches
 // (evict-first; with default stores the append of 16 k tokens took 94 us, not 91).
@@ -35,12 +37,14 @@ constexpr int kMaxTok = 8;                       // tokens per block at most
 constexpr int kUnits = kHeadDim / 16;            // two-piece units per head
 constexpr int kAhead = 4, kAppendAhead = 2;      // units whose loads a thread holds
 constexpr int kCsUnit = 9;                       // a unit's eight (cos, sin) and one of padding: no bank conflicts
-constexpr double kInvTwoPi = 0.15915494309189533577;
+constexpr double kTurnHi = 0x1.45f306dc9c883p-3, kTurnLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi), in two parts
 
-// Fraction of a turn of one position step, in units of 2^-64.
+// Fraction of a turn of one position step, in units of 2^-64 modulo 2^64: each part's distance to the
+// nearest whole number (exact), rounded to a unit.
 __device__ __forceinline__ unsigned long long turn_step(double f) {
-  const double t = f * kInvTwoPi;
-  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  const double hi = __dmul_rn(f, kTurnHi), lo = __fma_rn(f, kTurnLo, __fma_rn(f, kTurnHi, -hi));
+  return static_cast<unsigned long long>(__double2ll_rn((hi - rint(hi)) * 18446744073709551616.0)) +
+         static_cast<unsigned long long>(__double2ll_rn((lo - rint(lo)) * 18446744073709551616.0));
 }
 
 // cos and sin of pos * f, times m.
