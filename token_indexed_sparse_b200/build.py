@@ -1,26 +1,30 @@
 """Builds libqsa_b200.so (the CUDA kernels and the C ABI) in-tree with nvcc,
-and _qsa_torch.so (the short way from PyTorch tensors to it) with g++.
+and _qsa_torch.<tag>.so (the short way from PyTorch tensors to it) with g++.
 
     python -m token_indexed_sparse_b200.build [--force]
 
 The library is compiled for sm_100a only and links the CUDA runtime statically,
-so it carries no dependency on the runtime bundled with PyTorch; the binding is
-compiled against the PyTorch that imports it.
+so it carries no dependency on the runtime bundled with PyTorch, and it is built
+without one too.  The binding is compiled against the PyTorch that imports it; the
+tag in its name is that PyTorch's, so one built for another is never loaded.
+Without a binding the same calls go their longer way through Python.
 """
 
 from __future__ import annotations
 
+import hashlib
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqsa_b200.so")
-BINDING = os.path.join(PKG, "_qsa_torch.so")
 BINDING_SOURCE = os.path.join(CSRC, "qsa_torch.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
@@ -50,19 +54,27 @@ def up_to_date() -> bool:
     return _newer(LIB, _inputs())
 
 
-def build_binding(force: bool = False) -> str:
-    """Compiles _qsa_torch.so against the installed PyTorch."""
-    if not force and _newer(BINDING, [BINDING_SOURCE, os.path.join(INCLUDE, "qsa.h")]):
-        return BINDING
-    import sysconfig
+def binding_path() -> str:
+    """The binding's file for the installed PyTorch and Python."""
+    import torch
 
+    made_for = "|".join(str(x) for x in (torch.__version__, torch.version.git_version,
+                                         torch._C._GLIBCXX_USE_CXX11_ABI, sysconfig.get_config_var("SOABI")))
+    return os.path.join(PKG, f"_qsa_torch.{hashlib.sha256(made_for.encode()).hexdigest()[:12]}.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compiles the binding against the installed PyTorch; raises where that fails."""
+    binding = binding_path()
+    if not force and _newer(binding, [BINDING_SOURCE, os.path.join(INCLUDE, "qsa.h")]):
+        return binding
     import torch
     from torch.utils import cpp_extension
 
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
                 *cpp_extension.include_paths()]
-    tmp = BINDING + ".tmp"
+    tmp = binding + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{i}" for i in includes], BINDING_SOURCE, "-o", tmp,
@@ -71,12 +83,22 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, binding)
+    return binding
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_binding(force)
+    """The library, and the binding where there is a PyTorch that it compiles against (else a warning says so)."""
+    lib = build_library(force, verbose)
+    try:
+        build_binding(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"the library is built, the PyTorch binding is not (the paged-cache calls of qsa.py go their "
+                      f"longer way): {e}", RuntimeWarning, stacklevel=2)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

@@ -14,15 +14,17 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
 import operator
 import os
+import warnings
 
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqsa_b200.so")
 _lib = None
-_short = None  # _qsa_torch, bound to the library
+_short = None  # the compiled binding, bound to the library
 
 QSA_OK = 0
 
@@ -471,20 +473,45 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     return inv_freq.to(device), mscale
 
 
+class _NoShortWay:
+    """In place of the compiled binding where there is none for this PyTorch: takes nothing."""
+
+    @staticmethod
+    def rope(*args):
+        return NotImplemented
+
+    cache_append = paged_forward = paged_causal = rope
+
+
+def _load_binding():
+    from . import build
+
+    path = build.binding_path()
+    try:
+        spec = importlib.util.spec_from_file_location("_qsa_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:
+        warnings.warn(f"{os.path.basename(path)} does not load ({e}): the paged-cache calls go through Python, some "
+                      "10 us longer; build it with `python -m token_indexed_sparse_b200.build`", RuntimeWarning,
+                      stacklevel=4)
+        return None
+
+
 def _short_way():
-    """``_qsa_torch`` with the library's entry points (loads both once)."""
+    """The compiled binding with the library's entry points (loads both once), or what takes nothing."""
     global _short
     if _short is None:
         lib = library()
-        try:
-            from . import _qsa_torch
-        except ImportError as e:
-            raise RuntimeError("_qsa_torch.so does not load; build it with "
-                               "`python -m token_indexed_sparse_b200.build`") from e
-        _qsa_torch.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.qsa_rope, lib.qsa_cache_append, lib.qsa_paged_forward, lib.qsa_paged_forward_workspace_size,
-            lib.qsa_paged_causal, lib.qsa_paged_causal_workspace_size)))
-        _short = _qsa_torch
+        short = _load_binding()
+        if short is None:
+            short = _NoShortWay()
+        else:
+            short.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.qsa_rope, lib.qsa_cache_append, lib.qsa_paged_forward, lib.qsa_paged_forward_workspace_size,
+                lib.qsa_paged_causal, lib.qsa_paged_causal_workspace_size)))
+        _short = short
     return _short
 
 
