@@ -446,10 +446,14 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
 
     Pair i turns by ``base ** (-2 i / rotary_dim)`` per position.  ``scaling``
     for contexts ``factor`` times ``original_len``: ``"linear"`` divides every
-    frequency by the factor; ``"yarn"`` (Peng et al., 2023) divides those of
-    pairs with fewer than ``slow_turns`` turns over the original length, keeps
-    those with more than ``fast_turns``, goes linearly in the number of pairs
-    between, and grows q and k by ``0.1 ln(factor) + 1``."""
+    frequency by the factor; ``"yarn"`` (Peng et al., 2023) divides those of slow
+    pairs, keeps those of fast ones, and grows q and k by ``0.1 ln(factor) + 1``.
+
+    Between the two, the divided share grows linearly with the pair's index, as in
+    the models published with this scaling; the paper's own ramp is linear in the
+    turns that a pair makes over the original length, which gives other values.  It
+    starts at the last whole index (0 at least) whose pair makes ``fast_turns`` turns
+    or more and ends at the first whose pair makes ``slow_turns`` or fewer."""
     if rotary_dim < 16 or rotary_dim > 256 or rotary_dim % 16:
         raise ValueError("rotary_dim must be a multiple of 16, at most 256")
     if not base > 1.0 or not factor >= 1.0:
@@ -459,14 +463,18 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     if scaling == "linear":
         inv_freq = inv_freq / factor
     elif scaling == "yarn":
-        def pair(turns):  # the (real) pair index that makes this many turns over the original length
-            return rotary_dim * math.log(original_len / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
         if not fast_turns > slow_turns > 0.0 or original_len < 1:
             raise ValueError("yarn needs fast_turns > slow_turns > 0 and original_len >= 1")
-        lo, hi = math.floor(pair(fast_turns)), math.ceil(pair(slow_turns))
-        lo, hi = max(lo, 0), min(hi, rotary_dim - 1)
-        slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
-        inv_freq = inv_freq * (1.0 - slow) + inv_freq / factor * slow
+
+        def index(turns):  # where base ** (-2 index / rotary_dim) * original_len is 2 pi turns
+            return rotary_dim * math.log(original_len / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
+
+        kept, divided = max(math.floor(index(fast_turns)), 0), math.ceil(index(slow_turns))
+        if divided > kept:
+            share = ((i - kept) / (divided - kept)).clamp(0.0, 1.0)
+        else:  # even pair 0 makes no more than slow_turns
+            share = torch.ones_like(i)
+        inv_freq = inv_freq * (1.0 - share) + inv_freq / factor * share
         mscale = 0.1 * math.log(factor) + 1.0
     elif scaling is not None:
         raise ValueError('scaling must be None, "linear" or "yarn"')
