@@ -78,3 +78,15 @@ def test_the_workspace_sizes_refuse_what_32_bits_do_not_hold(status):
     x = torch.zeros(1, 1, 256, dtype=torch.bfloat16).expand(1, 2**32 + 12, 256)
     with pytest.raises(ValueError, match="heads of q must fit 32 bits"):
         qsa.rope(x, None, torch.zeros(1, dtype=torch.int32), torch.ones(8, dtype=torch.float64))
+
+
+def test_the_status_word_is_the_workspace_s_first_int():
+    from token_indexed_sparse_b200 import qsa
+    ws = torch.zeros(512, dtype=torch.uint8)
+    w = qsa.status_word(ws)
+    assert w.dtype == torch.int32 and w.shape == (1,) and w.data_ptr() == ws.data_ptr()
+    ws[:4] = torch.tensor([2, 0, 0, 0], dtype=torch.uint8)
+    assert w.item() == 2
+    for bad in (ws.int(), ws[:2], ws[::2], ws.view(2, 256)):
+        with pytest.raises(ValueError, match="workspace"):
+            qsa.status_word(bad)

@@ -63,3 +63,14 @@ def test_angles_of_far_positions_and_fast_pairs(backward):
     # cosine and sine, one BF16 rounding
     tol = 2 * math.pi * 2.0**-25 + 2.0**-22 + 2.0**-8 * np.abs(ref)
     assert (np.abs(y[..., :16] - ref) <= tol).all()
+
+
+def test_the_status_word_says_that_no_wait_gave_up():
+    c = _cache([900, 20], [30, 1], 32, 1, 72)
+    r = _routes(c, 300, 2)
+    n = max(qsa.paged_causal_workspace_size(31, 12, 1, 32, c["table"].shape[1]),
+            qsa.paged_forward_workspace_size(31, 12, 1, 300, 32, c["table"].shape[1]))
+    for kw in (dict(), dict(window=50, sinks=2), dict(routes=r)):
+        ws = torch.full((n,), 0xAB, dtype=torch.uint8, device=DEV)
+        _check(c, *_attend(c, workspace=ws, **kw), **kw)
+        assert qsa.status_word(ws).item() == 0

@@ -730,6 +730,17 @@ def paged_causal_workspace_size(T, H, G, page_size, max_pages, window: int = 0, 
     return int(library().qsa_paged_causal_workspace_size(T, H, G, page_size, max_pages, window, sinks))
 
 
+def status_word(workspace: torch.Tensor) -> torch.Tensor:
+    """The status word of a call that was given ``workspace``: a one-element int32 view of it on the device.
+
+    Once the call's work has completed it is 0, or nonzero if a kernel gave up on a bounded wait
+    (the call's outputs are then invalid).  Nothing is read or waited for here: a program looks when
+    it synchronises anyway, before the workspace goes into another call."""
+    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous() or workspace.numel() < 4:
+        raise ValueError("workspace must be a contiguous uint8 vector")
+    return workspace[:4].view(torch.int32)
+
+
 def paged_forward(q, k_pages, v_pages, routes, block_table, kv_len, cu_q, scale: float = 1.0 / 16.0, *, out=None,
                   lse=None, workspace=None):
     """qsa_paged_forward: ``(out [T, H, 256] bf16, lse [T, H] float32)`` of new tokens over a paged cache.
@@ -763,7 +774,9 @@ def paged_causal(q, k_pages, v_pages, block_table, kv_len, cu_q, scale: float = 
 
     A token at position p sees the positions ``j <= p`` of its sequence, with
     ``window`` above 0 only those with ``j > p - window`` or ``j < sinks``.  The
-    cache as in ``paged_forward``."""
+    cache as in ``paged_forward``.  The kernel's waits are bounded; a caller who wants to
+    see that none gave up brings a ``workspace`` (``paged_causal_workspace_size``) and
+    looks at its ``status_word``."""
     r = (_short or _short_way()).paged_causal(q, k_pages, v_pages, block_table, kv_len, cu_q, scale, window, sinks, out,
                                               lse, workspace)
     if r is not NotImplemented:
