@@ -486,11 +486,13 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     t_end = n_tiles * (c + 1) / n_ctas;
     auto locate = [&](int seq, int i, long long w, long long at) {  // if the range begins in this query tile
       if (t_begin < at || t_begin >= at + w) return;
-      const long long n = w / a.G, off = t_begin - at;  // key tiles of all groups may pass 31 bits
+      const int n = static_cast<int>(w / a.G);
+      const long long off = t_begin - at;  // of the key tiles of all groups, which may pass 31 bits
+      const int g = off <= 0x7fffffff ? static_cast<int>(off) / n : static_cast<int>(off / n);
       start[0] = seq;
       start[1] = i;
-      start[2] = static_cast<int>(off / n);
-      start[3] = static_cast<int>(off - off / n * n);
+      start[2] = g;
+      start[3] = static_cast<int>(off - static_cast<long long>(g) * n);
     };
     if (batches == 1) {  // what the scan above has in hand
       locate(seq0, tile0, w0, incl0 - w0);
