@@ -4,8 +4,15 @@
 // over them, the 12 heads of a (token, KV group) pair at a time (softmax of scaled dot products with
 // a running maximum that may lag by 2^8, P rounded to BF16 for P V, FP32 sums; empty rows give zero
 // output and -inf LSE): chunks of 16 keys through a two-stage ring of 16-byte cp.async copies, four
-// CTAs of two warps per SM.  Rows outside the set are never read, whatever they hold.  Bound by the
-// gather: 1 KB of K and V per (token, key, group), mostly from L2.
+// CTAs of two warps per SM.  Rows outside the set are never read, whatever they hold.
+//
+// A (token, key, group) costs 1 KB of K and V.  The gather runs at 30 B/clk/SM (512 tokens with 2048 routes
+// over 131072: 139 us, L2 hit rate 41 %, DRAM 3.9 TB/s; 2048 tokens: 464 us), where a bare cp.async gather
+// reaches 46 from L2 with 8 warps an SM and 25, the HBM limit, past it.  At those 8 warps, all that 254 registers
+// a thread leave, the instructions of a 16-key chunk set the pace (413 a warp at 4.3 cycles each).
+//
+// P is BF16 because the tensor cores take P and V in one type, and V is BF16: a relative 2^-8 a term at most,
+// 2.3e-3 of an output against 64 bits where rounding the output alone gives 1.7e-3.  Row sums are taken before it.
 //
 // Few tokens (a decode step) leave most SMs idle when one CTA takes a whole list, so a list is cut
 // into `splits` parts whose unnormalised sums go to a workspace, and a second kernel joins them in

@@ -23,7 +23,7 @@
 // of its units, then the block computes the cosines and sines of its (token, pair)s
 // into shared memory for all heads, then each thread rotates its units in FP32 and
 // rounds once.  A unit is two 16-byte pieces of one head that hold eight whole pairs
-// in either layout.  26 heads of 32768 tokens: 138 us, 6.3 TB/s (133 us at the rate
+// in either layout.  26 heads of 32768 tokens: 139 us, 6.3 TB/s (133 us at the rate
 // of a plain copy).
 #include "qsa_cache.cuh"
 #include "qsa_device.cuh"
