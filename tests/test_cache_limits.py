@@ -1,6 +1,7 @@
 """Sizes at the limits of the paged-cache calls: refused on the host, before any
-CUDA work, where the kernels' 32-bit counts would not hold them.  Each call runs
-in a process of its own, so that one which ends the process fails its test only."""
+CUDA work, where the kernels' 32-bit counts would not hold them.  The calls run in a
+process of their own, so that one which ends the process fails its test (and those
+behind it) only."""
 
 import subprocess
 import sys
@@ -25,37 +26,37 @@ def append(T, G, B=1, q=None):
 """
 
 
+CAUSAL = "lib.qsa_paged_causal(*[P(256)] * 6, 8, {B}, 4, 16, 3, 12, 1, 0, 0, 1.0, *[P(256)] * 3, 1 << 40, None)"
+ROUTED = "lib.qsa_paged_forward(*[P(256)] * 7, 8, {B}, 4, 16, 3, 12, 1, 4, 1.0, *[P(256)] * 3, 1 << 40, None)"
+
+# 16 units a head, and 1024 behind them, have to fit 31 bits
+HEADS = ["rope(1, 2**28, 0)", "rope(1, 2**28 - 1, 1)", "rope(1, 2**27, 0)", "rope(1, 2**27 - 64, 0)",
+         "rope(1, 2**26, 2**26)", "rope(1, 2**31 - 1, 0)", "append(1, 2**27)", "append(1, 2**31 // 14)",
+         "append(1, 2**27 // 14)", "append(1, 2**27 // 14, q=1 << 40)"]
+# the search for a row's sequence looks up to 31 offsets past B, the plan up to 383
+SEQUENCES = [call.format(B=B) for call in ("append(8, 1, {B})", CAUSAL, ROUTED)
+             for B in ("2**31 - 1", "2**31 - 384", "2**30 + 1")]
+
+
 @pytest.fixture(scope="module")
 def status():
     from token_indexed_sparse_b200 import build
     build.build()
-
-    def run(call):
-        r = subprocess.run([sys.executable, "-c", f"{HEAD}\nprint('status', {call})"], capture_output=True, text=True)
-        assert r.returncode == 0, f"the process ended with {r.returncode}: {r.stderr}"
-        return int(r.stdout.split("status")[1])
-
-    return run
+    code = "".join(f"\nprint('status', {call}, flush=True)" for call in HEADS + SEQUENCES)
+    r = subprocess.run([sys.executable, "-c", HEAD + code], capture_output=True, text=True)
+    found = [int(line.split()[1]) for line in r.stdout.splitlines() if line.startswith("status")]
+    return {call: found[i] if i < len(found) else f"the process ended with {r.returncode}: {r.stderr}"
+            for i, call in enumerate(HEADS + SEQUENCES)}
 
 
-# 16 units a head, and 1024 behind them, have to fit 31 bits
-@pytest.mark.parametrize("call", ["rope(1, 2**28, 0)", "rope(1, 2**28 - 1, 1)", "rope(1, 2**27, 0)",
-                                  "rope(1, 2**27 - 64, 0)", "rope(1, 2**26, 2**26)", "rope(1, 2**31 - 1, 0)",
-                                  "append(1, 2**27)", "append(1, 2**31 // 14)", "append(1, 2**27 // 14)",
-                                  "append(1, 2**27 // 14, q=1 << 40)"])
+@pytest.mark.parametrize("call", HEADS)
 def test_heads_past_the_kernels_counts_are_refused(status, call):
-    assert status(call) == 1
+    assert status[call] == 1
 
 
-CAUSAL = "lib.qsa_paged_causal(*[P(256)] * 6, 8, {B}, 4, 16, 3, 12, 1, 0, 0, 1.0, *[P(256)] * 3, 1 << 40, None)"
-ROUTED = "lib.qsa_paged_forward(*[P(256)] * 7, 8, {B}, 4, 16, 3, 12, 1, 4, 1.0, *[P(256)] * 3, 1 << 40, None)"
-
-
-# the search for a row's sequence looks up to 31 offsets past B, the plan up to 383
-@pytest.mark.parametrize("B", ["2**31 - 1", "2**31 - 384", "2**30 + 1"])
-@pytest.mark.parametrize("call", ["append(8, 1, {B})", CAUSAL, ROUTED])
-def test_more_sequences_than_the_searches_count_are_refused(status, call, B):
-    assert status(call.format(B=B)) == 1
+@pytest.mark.parametrize("call", SEQUENCES)
+def test_more_sequences_than_the_searches_count_are_refused(status, call):
+    assert status[call] == 1
 
 
 @pytest.mark.parametrize("name", ["window", "sinks"])
