@@ -605,7 +605,7 @@ causal_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
       }
       if (ok) load_v(prev);
     }
-    if (!ok && lane == 0) {  // copies in flight end before the block does (bounded)
+    if (lane == 0) {  // copies in flight end before the block does, whoever has given up meanwhile (bounded)
       Ring r = ring;
       for (uint32_t i = 0; i < min(issued, static_cast<uint32_t>(kUnits)); ++i) {
         if (--r.slot < 0) {
