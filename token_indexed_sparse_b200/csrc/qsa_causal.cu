@@ -32,7 +32,7 @@
 // instruction, not 64.  A decode step is bound by the cache's bytes (48 sequences of up to
 // 32768 tokens: 0.27 ms, 6.3 TB/s), a long chunk by the time from S to P and back, about
 // 3200 cycles a tile, and by the power cap when kept up (2048 tokens behind 30000, 24 heads:
-// 1.23 to 1.26 ms, 1.2 to 1.3 PFLOP/s in a burst, 1.42 to 1.48 ms kept up; in 1024 behind 16000,
+// 1.23 to 1.26 ms, 1.2 to 1.3 PFLOP/s in a burst, 1.40 to 1.48 ms kept up; in 1024 behind 16000,
 // tensor pipe 64 % active, MUFU 32 %).  Short items (a window of 1021: 131 us for 39 us of operations,
 // tensor pipe 33 %) by their starts, ends and edge tiles.
 //
